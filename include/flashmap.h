@@ -63,6 +63,9 @@ typedef enum { FLASHMAP_F32 = 0, FLASHMAP_BF16 = 1, FLASHMAP_E4M3 = 2 } flashmap
 #define FLASHMAP_DEVERR_TOKEN 4u     /* an anchor token id outside [0, vocab_size) */
 #define FLASHMAP_DEVERR_TIMEOUT 8u   /* a pipeline wait gave up (kernel returned early) */
 #define FLASHMAP_DEVERR_NUMERIC 16u  /* a non-positive pivot in the load-time Cholesky */
+#define FLASHMAP_DEVERR_CAPACITY 32u /* the free-page list or an output's rows ran out */
+#define FLASHMAP_DEVERR_TREE 64u     /* a node count outside [0, width], or an id naming no earlier node */
+#define FLASHMAP_DEVERR_REQUEST 128u /* a page-table row out of range, named twice, or holding too few pages */
 
 /*
  * FlashMapConfig (flashmap/configuration_flashmap.py, FlashMapConfig) restricted to
@@ -389,6 +392,135 @@ flashmap_status flashmap_draft_candidates(flashmap_model* model, const flashmap_
 flashmap_status flashmap_build_tree(const int64_t* candidates, int32_t bs, int32_t n_cand, int32_t block_size,
                                     int32_t width, int64_t* tokens_out, int64_t* ids_out, int64_t* stats_out,
                                     flashmap_stream stream);
+
+/* ----------------------------------------------------------------------------------
+ * Verifying a drafted tree on the target's side. A serving loop that has drafted with
+ * the calls above lets the target check the tree: flashmap_extend_pages gives the tree's
+ * nodes pages and slots of the target's cache, the target's layers write the nodes' keys
+ * and values there and call flashmap_tree_attention, and flashmap_sample_filtered draws
+ * the target's tokens from its logits. The pages have no counterpart (their servers
+ * bring these three); they are library-level additions. They take no model: the target's
+ * cache has its own head counts. Device-side checks report into `dev_err` (device, one
+ * uint32 the caller zeroes and reads; FLASHMAP_DEVERR_* bits are ORed in), or nowhere
+ * when it is NULL.
+ * ---------------------------------------------------------------------------------- */
+
+/*
+ * Page tables and slot maps from request lengths, on the GPU, with no host sync. Request
+ * b (page-table row req_pool_idx[b], lens[b] cached positions, held[b] pages) gets
+ * new_lens[b] tokens. Its row is extended by
+ *   need[b] = max(0, ceil((lens[b] + new_lens[b]) / page_size) - held[b])
+ * pages, taken in request order from free_pages[*free_head ...] and entered at columns
+ * held[b]...; token t of the request is output row cu_tokens[b] + t, at position
+ * lens[b] + t and slot page * page_size + position % page_size.
+ *   req_pool_idx, lens, new_lens (device) int32 [bs]; no page-table row twice
+ *   held             (device) int32 [bs], at least ceil(lens / page_size); more when pages
+ *                    reserved for rejected tokens are still in the row; NULL: just that
+ *   req_to_page      (device) int32 [table_rows][req_to_page_stride], updated in place;
+ *                    entries other than the new pages' are left as they were
+ *   free_pages       (device) int32 [num_free]; free_head (device) int32 [1]: the entries
+ *                    already handed out
+ *   free_head_out    (device) int32 [1] the same after this call
+ *   held_out         (device) int32 [bs] held[b] + need[b], or NULL
+ *   num_pages        the pool's pages: ids outside [0, num_pages) are not entered
+ *   cu_tokens        (device) int32 [bs + 1] prefix sum of new_lens
+ *   slots            (device) int64 [max_tokens]; positions, token_req (the request b of
+ *                    each row) (device) int32 [max_tokens] or NULL. Rows from
+ *                    cu_tokens[bs] on are left as they were.
+ * Inputs are only read, so the same call repeated (a replayed graph) does the same again;
+ * free_head_out and held_out must not be the buffers free_head and held: they may be the
+ * next call's. A request that cannot be served (a length below zero or a position past its
+ * row: POSITION; its row out of range, named by an earlier request of the batch, or holding
+ * fewer pages than lens needs: REQUEST; its rows past max_tokens, or its pages past the free
+ * list's end: CAPACITY) gets no page, slots -1, and its held pages back as held_out; a
+ * negative new_lens counts as no tokens. A bad page id leaves slots -1 (PAGE). Limits:
+ * bs <= 8192, table_rows <= 32768.
+ */
+flashmap_status flashmap_extend_pages(int32_t bs, const int32_t* req_pool_idx, const int32_t* lens,
+                                      const int32_t* new_lens, const int32_t* held, int32_t page_size,
+                                      int32_t* req_to_page, int32_t table_rows, int32_t req_to_page_stride,
+                                      const int32_t* free_pages, int32_t num_free, const int32_t* free_head,
+                                      int32_t* free_head_out, int32_t* held_out, int64_t num_pages,
+                                      int32_t max_tokens, int32_t* cu_tokens, int64_t* slots, int32_t* positions,
+                                      int32_t* token_req, uint32_t* dev_err, flashmap_stream stream);
+
+/* One layer of a paged cache: keys and values (device, 16-byte aligned), each
+ * [num_pages][num_kv_heads][page_size][head_dim] in dtype (F32 or BF16), the layout of one
+ * layer's keys or values in a flashmap_kv_pool. page_size a multiple of 16; head_dim 32,
+ * 64 or 128. */
+typedef struct {
+  const void *keys, *values;
+  int64_t num_pages;
+  int32_t num_kv_heads, page_size, head_dim, dtype;
+} flashmap_cache_layer;
+
+/* Workspace bytes of flashmap_tree_attention for these sizes (current device). */
+flashmap_status flashmap_tree_attention_workspace(const flashmap_cache_layer* cache, int32_t bs, int32_t width,
+                                                  int32_t num_heads, size_t* bytes);
+
+/*
+ * Attention of a tree of drafted tokens over the cache. Request b has ctx_lens[b] cached
+ * positions before its tree; node i of the tree (0 is the root, the anchor) has its key
+ * and value in the cache at position ctx_lens[b] + i and sees the positions below
+ * ctx_lens[b], its ancestors and itself:
+ *   out = softmax(scale * q k^T) v over those, query head h reading key/value head
+ *   h / (num_heads / num_kv_heads).
+ *   q            (device, 16-byte aligned) node i of request b at q + (b * width + i) *
+ *                q_stride elements, [num_heads][head_dim] in the cache's dtype; q_stride a
+ *                multiple of 16 bytes, at least num_heads * head_dim
+ *   num_nodes    (device) int32 [bs] nodes of each request in [0, width], or NULL: width.
+ *                Rows of out past them are left as they were.
+ *   tree_ids     (device) int64 [bs][width - 1] parent * width + i for nodes i = 1.., as
+ *                flashmap_build_tree writes them, or NULL: a chain (one drafted block;
+ *                width 1: single tokens)
+ *   req_pool_idx (device) int32 [bs]; req_to_page (device) int32 [table_rows][stride]
+ *   out          (device, 16-byte aligned) [bs * width][num_heads][head_dim]
+ * Scores, the softmax and its sums are float32; with BF16 the probabilities are rounded to
+ * bf16 for their product with the values. Cached keys and values of visible positions must
+ * be finite or give NaN; positions past a request's last node are not read into results.
+ * Device checks: a page id out of range or a position past the table's stride hides the
+ * position (PAGE, POSITION); a request with a bad table row or negative ctx_lens is skipped
+ * (REQUEST, POSITION), its rows of out left as they were; a node whose id names no earlier
+ * node sees the context and itself (TREE); a row that sees nothing is 0. Limits: width <=
+ * 1025, num_heads a multiple of num_kv_heads, num_pages * num_kv_heads * page_size < 2^31.
+ */
+flashmap_status flashmap_tree_attention(const flashmap_cache_layer* cache, const void* q, int64_t q_stride,
+                                        int32_t bs, int32_t width, int32_t num_heads, const int32_t* ctx_lens,
+                                        const int32_t* num_nodes, const int64_t* tree_ids,
+                                        const int32_t* req_pool_idx, const int32_t* req_to_page, int32_t table_rows,
+                                        int32_t req_to_page_stride, float scale, void* out, void* workspace,
+                                        size_t workspace_bytes, uint32_t* dev_err, flashmap_stream stream);
+
+/*
+ * One token per row under temperature, top-k, top-p and min-p, from a given uniform. Row r
+ * belongs to request b = r / rows_per_request. In the order (logit descending, index
+ * ascending) and with w_j = exp((l_j - max l) / temperature[b]):
+ *   top_k[b]  keeps the first top_k entries                  (off: <= 0 or >= vocab)
+ *   top_p[b]  then keeps the entries before which less than top_p of the kept mass lies, the
+ *             first one always                               (off: >= 1 or NaN)
+ *   min_p[b]  then keeps the entries with w_j >= min_p       (off: <= 0 or NaN; above 1: 1)
+ * and the token is the lowest index j with sum_{kept i <= j} w_i > u * (kept mass).
+ * temperature <= 0 (or NaN) takes the largest logit, the lowest index on ties. Logits of
+ * -inf or NaN are never drawn; a row of nothing else gives index 0 with probability 0.
+ * The weights are taken as multiples of 2^-44 (an entry whose weight rounds to none is never
+ * drawn, even at u = 0) and summed exactly: a row's token does not depend on the other rows,
+ * the launch or the order of the sums.
+ *   logits      (device) [rows] rows of vocab F32 or BF16 entries, ld entries apart
+ *   temperature (device) float32, top_k int32, top_p, min_p float32, per request; the last
+ *               three may be NULL: off
+ *   uniforms    (device) float32 [rows] in [0, 1); other values are clamped into it
+ *   ids         (device) int64 [vocab] the token of each index (a draft vocabulary's hot
+ *               tokens), or NULL: the index
+ *   tokens_out  (device) int64 [rows]
+ *   probs_out   (device) float32 [rows] the token's probability among the kept entries (1
+ *               when greedy), or NULL
+ * Limits: vocab <= 393216.
+ */
+flashmap_status flashmap_sample_filtered(const void* logits, int32_t dtype, int32_t rows, int32_t vocab, int64_t ld,
+                                         int32_t rows_per_request, const float* temperature, const int32_t* top_k,
+                                         const float* top_p, const float* min_p, const float* uniforms,
+                                         const int64_t* ids, int64_t* tokens_out, float* probs_out,
+                                         flashmap_stream stream);
 
 /* The device error word (FLASHMAP_DEVERR_* bits), then clears it. Synchronizes
  * `stream`. Returns E_DEVICE when the word was non-zero. */

@@ -19,7 +19,8 @@ HEADER = os.path.join(os.path.dirname(HERE), "include", "flashmap.h")
 F32, BF16, E4M3 = 0, 1, 2
 DTYPE_CODES = {"f32": F32, "bf16": BF16, "e4m3": E4M3}
 STATUS = {0: "OK", 1: "E_INVALID", 2: "E_UNSUPPORTED", 3: "E_CUDA", 4: "E_NOMEM", 5: "E_DEVICE"}
-DEVERR = {"PAGE": 1, "POSITION": 2, "TOKEN": 4, "TIMEOUT": 8, "NUMERIC": 16}
+DEVERR = {"PAGE": 1, "POSITION": 2, "TOKEN": 4, "TIMEOUT": 8, "NUMERIC": 16, "CAPACITY": 32, "TREE": 64,
+          "REQUEST": 128}
 
 _c = ctypes
 _vp = _c.c_void_p
@@ -78,6 +79,11 @@ class flashmap_pending_write(_c.Structure):
                 ("out_loc", _vp)]
 
 
+class flashmap_cache_layer(_c.Structure):
+    _fields_ = [("keys", _vp), ("values", _vp), ("num_pages", _c.c_int64)] + \
+        [(n, _c.c_int32) for n in ("num_kv_heads", "page_size", "head_dim", "dtype")]
+
+
 class flashmap_launch_record(_c.Structure):
     _fields_ = [("kind", _c.c_int32), ("layer", _c.c_int32), ("rows", _c.c_int32), ("n", _c.c_int32),
                 ("k", _c.c_int32), ("ms", _c.c_float)]
@@ -130,6 +136,16 @@ def lib():
         L.flashmap_profile_gemm_chain.argtypes = [_vp, _c.c_int32, _c.c_int32, _vp, _vp, _c.c_size_t,
                                                   P(_c.c_int64), P(_c.c_int32), _vp]
         L.flashmap_build_tree.argtypes = [_vp, _c.c_int32, _c.c_int32, _c.c_int32, _c.c_int32, _vp, _vp, _vp, _vp]
+        L.flashmap_extend_pages.argtypes = [_c.c_int32, _vp, _vp, _vp, _vp, _c.c_int32, _vp, _c.c_int32, _c.c_int32,
+                                            _vp, _c.c_int32, _vp, _vp, _vp, _c.c_int64, _c.c_int32, _vp, _vp, _vp, _vp,
+                                            _vp, _vp]
+        L.flashmap_tree_attention_workspace.argtypes = [P(flashmap_cache_layer), _c.c_int32, _c.c_int32, _c.c_int32,
+                                                        P(_c.c_size_t)]
+        L.flashmap_tree_attention.argtypes = [P(flashmap_cache_layer), _vp, _c.c_int64, _c.c_int32, _c.c_int32,
+                                              _c.c_int32, _vp, _vp, _vp, _vp, _vp, _c.c_int32, _c.c_int32, _c.c_float,
+                                              _vp, _vp, _c.c_size_t, _vp, _vp]
+        L.flashmap_sample_filtered.argtypes = [_vp, _c.c_int32, _c.c_int32, _c.c_int32, _c.c_int64, _c.c_int32, _vp,
+                                               _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]
         L.flashmap_draft_candidates.argtypes = [_vp, P(flashmap_kv_pool), _c.c_int32, _c.c_int32, _vp, _vp, _vp, _vp,
                                                 _c.c_int32, _vp, _c.c_float, _vp, _vp, _vp, _c.c_size_t, _vp]
         L.flashmap_profile_start.argtypes = [_vp, _c.c_int32]
@@ -297,6 +313,92 @@ def flashmap_build_tree(candidates, width: int, tokens_out, ids_out, stats_out, 
     bs, n, k = candidates.shape
     _check(lib().flashmap_build_tree(_ptr(candidates), int(bs), int(n), int(k), int(width), _ptr(tokens_out),
                                      _ptr(ids_out), _ptr(stats_out), _stream(stream)))
+
+
+def _dense(name: str, t, dtype: str, n: int | None = None):
+    """Checks that t is a contiguous CUDA tensor of this dtype (and of n elements at least); its pointer."""
+    if t is None:
+        return None
+    if not t.is_cuda or str(t.dtype)[6:] != dtype or not t.is_contiguous() or (n is not None and t.numel() < n):
+        raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor" +
+                         (f" of at least {n} elements" if n is not None else ""))
+    return t.data_ptr()
+
+
+def flashmap_extend_pages(req_pool_idx, lens, new_lens, held, page_size: int, req_to_page, free_pages, free_head,
+                          free_head_out, held_out, num_pages: int, cu_tokens, slots, positions=None, token_req=None,
+                          dev_err=None, stream=None) -> None:
+    """Extends req_to_page (rows, stride) in place; slots' length is the most tokens a call may have."""
+    bs, most = req_pool_idx.numel(), slots.numel()
+    if req_to_page.dim() != 2:
+        raise ValueError("req_to_page must be (rows, stride)")
+    rows, stride = req_to_page.shape
+    _check(lib().flashmap_extend_pages(
+        bs, _dense("req_pool_idx", req_pool_idx, "int32"), _dense("lens", lens, "int32", bs),
+        _dense("new_lens", new_lens, "int32", bs), _dense("held", held, "int32", bs), page_size,
+        _dense("req_to_page", req_to_page, "int32"), rows, stride, _dense("free_pages", free_pages, "int32"),
+        free_pages.numel(), _dense("free_head", free_head, "int32", 1),
+        _dense("free_head_out", free_head_out, "int32", 1), _dense("held_out", held_out, "int32", bs), num_pages, most,
+        _dense("cu_tokens", cu_tokens, "int32", bs + 1), _dense("slots", slots, "int64"),
+        _dense("positions", positions, "int32", most), _dense("token_req", token_req, "int32", most),
+        _dense("dev_err", dev_err, "int32", 1), _stream(stream)))
+
+
+def make_cache_layer(keys, values) -> flashmap_cache_layer:
+    """One layer's paged keys and values, each (num_pages, num_kv_heads, page_size, head_dim)."""
+    kind = str(keys.dtype)[6:]
+    if keys.dim() != 4 or keys.shape != values.shape or kind not in ("float32", "bfloat16"):
+        raise ValueError("keys and values must be float32 or bfloat16 (num_pages, num_kv_heads, page_size, head_dim)")
+    pages, heads, page, hd = keys.shape
+    c = flashmap_cache_layer(_dense("keys", keys, kind), _dense("values", values, kind), pages, heads, page, hd,
+                             F32 if kind == "float32" else BF16)
+    c.kind, c._keep = kind, (keys, values)
+    return c
+
+
+def flashmap_tree_attention_workspace(cache: flashmap_cache_layer, bs: int, width: int, num_heads: int) -> int:
+    n = _c.c_size_t()
+    _check(lib().flashmap_tree_attention_workspace(_c.byref(cache), int(bs), int(width), int(num_heads), _c.byref(n)))
+    return n.value
+
+
+def flashmap_tree_attention(cache: flashmap_cache_layer, q, width: int, ctx_lens, num_nodes, tree_ids, req_pool_idx,
+                            req_to_page, scale: float, out, workspace, dev_err=None, stream=None) -> None:
+    """q (bs * width, num_heads, head_dim), its rows possibly further apart (a slice of a wider
+    projection); out the same shape, contiguous; tree_ids (bs, width - 1) from flashmap_build_tree or None."""
+    bs, heads, hd = ctx_lens.numel(), q.shape[1], q.shape[2]
+    if not q.is_cuda or str(q.dtype)[6:] != cache.kind or q.shape[0] != bs * width or hd != cache.head_dim or \
+            q.stride(2) != 1 or q.stride(1) != hd:
+        raise ValueError("q must be (bs * width, num_heads, head_dim) in the cache's dtype with dense rows")
+    if req_to_page.dim() != 2:
+        raise ValueError("req_to_page must be (rows, stride)")
+    rows, stride = req_to_page.shape
+    _check(lib().flashmap_tree_attention(
+        _c.byref(cache), q.data_ptr(), q.stride(0) if bs * width > 1 else heads * hd, bs, width, heads,
+        _dense("ctx_lens", ctx_lens, "int32"), _dense("num_nodes", num_nodes, "int32", bs),
+        _dense("tree_ids", tree_ids, "int64", bs * (width - 1)), _dense("req_pool_idx", req_pool_idx, "int32", bs),
+        _dense("req_to_page", req_to_page, "int32"), rows, stride, scale,
+        _dense("out", out, cache.kind, bs * width * heads * hd), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _dense("dev_err", dev_err, "int32", 1), _stream(stream)))
+
+
+def flashmap_sample_filtered(logits, rows_per_request: int, temperature, top_k, top_p, min_p, uniforms, ids,
+                             tokens_out, probs_out=None, stream=None) -> None:
+    """logits (rows, vocab) float32 or bfloat16, rows possibly further apart than vocab; top_k, top_p,
+    min_p, ids and probs_out may be None."""
+    kind = str(logits.dtype)[6:]
+    if not logits.is_cuda or logits.dim() != 2 or kind not in ("float32", "bfloat16") or logits.stride(1) != 1:
+        raise ValueError("logits must be a CUDA float32 or bfloat16 (rows, vocab) tensor with dense rows")
+    rows, vocab = logits.shape
+    bs = -(-rows // max(1, rows_per_request))
+    _check(lib().flashmap_sample_filtered(
+        logits.data_ptr(), F32 if kind == "float32" else BF16, rows, vocab,
+        logits.stride(0) if rows > 1 else vocab,
+        rows_per_request, _dense("temperature", temperature, "float32", bs), _dense("top_k", top_k, "int32", bs),
+        _dense("top_p", top_p, "float32", bs), _dense("min_p", min_p, "float32", bs),
+        _dense("uniforms", uniforms, "float32", rows), _dense("ids", ids, "int64", vocab),
+        _dense("tokens_out", tokens_out, "int64", rows), _dense("probs_out", probs_out, "float32", rows),
+        _stream(stream)))
 
 
 def flashmap_get_device_error(model: Model, stream=None) -> int:

@@ -1487,6 +1487,140 @@ flashmap_status flashmap_build_tree(const int64_t* candidates, int32_t bs, int32
   return FLASHMAP_OK;
 }
 
+// ------------------------------------------------------------------ verifying a tree (no model)
+
+namespace {
+
+flashmap_status current_launch(flashmap_stream stream, uint32_t* dev_err, Launch* L) {
+  int dev = 0, sms = 0;
+  FM_CUDA(cudaGetDevice(&dev));
+  FM_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+  *L = Launch{reinterpret_cast<cudaStream_t>(stream), sms, dev_err, true};
+  return FLASHMAP_OK;
+}
+
+flashmap_status check_cache_layer(const flashmap_cache_layer* c, int bs, int width, int num_heads) {
+  if (!c) return fail(FLASHMAP_E_INVALID, "cache is NULL");
+  if (c->num_pages <= 0 || c->num_kv_heads <= 0 || c->page_size <= 0 || c->head_dim <= 0 || bs <= 0 || width <= 0 ||
+      num_heads <= 0)
+    return fail(FLASHMAP_E_INVALID, "every size must be positive");
+  if (c->dtype == FLASHMAP_E4M3) return fail(FLASHMAP_E_UNSUPPORTED, "the cache must be F32 or BF16");
+  if (!is_act(c->dtype)) return fail(FLASHMAP_E_INVALID, "bad cache dtype");
+  if (c->page_size % 16) return fail(FLASHMAP_E_UNSUPPORTED, "page_size must be a multiple of 16");
+  if (c->head_dim != 32 && c->head_dim != 64 && c->head_dim != 128)
+    return fail(FLASHMAP_E_UNSUPPORTED, "head_dim must be 32, 64 or 128");
+  if (num_heads % c->num_kv_heads) return fail(FLASHMAP_E_INVALID, "num_heads must be a multiple of num_kv_heads");
+  if (width > fm::kTreeMaxNodes + 1) return fail(FLASHMAP_E_UNSUPPORTED, "width must be <= 1025");
+  if (c->num_pages > INT32_MAX / c->page_size / c->num_kv_heads)
+    return fail(FLASHMAP_E_UNSUPPORTED, "num_pages * num_kv_heads * page_size must be below 2^31");
+  if (num_heads > 65536 || bs > (1 << 20) || static_cast<int64_t>(bs) * width > INT32_MAX / 2)
+    return fail(FLASHMAP_E_UNSUPPORTED, "too many heads or rows");
+  return FLASHMAP_OK;
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+}  // namespace
+
+flashmap_status flashmap_extend_pages(int32_t bs, const int32_t* req_pool_idx, const int32_t* lens,
+                                      const int32_t* new_lens, const int32_t* held, int32_t page_size,
+                                      int32_t* req_to_page, int32_t table_rows, int32_t req_to_page_stride,
+                                      const int32_t* free_pages, int32_t num_free, const int32_t* free_head,
+                                      int32_t* free_head_out, int32_t* held_out, int64_t num_pages,
+                                      int32_t max_tokens, int32_t* cu_tokens, int64_t* slots, int32_t* positions,
+                                      int32_t* token_req, uint32_t* dev_err, flashmap_stream stream) {
+  g_last_error.clear();
+  if (!req_pool_idx || !lens || !new_lens || !req_to_page || !free_head || !free_head_out || !cu_tokens)
+    return fail(FLASHMAP_E_INVALID, "NULL argument");
+  if (num_free < 0 || max_tokens < 0 || (num_free > 0 && !free_pages) || (max_tokens > 0 && !slots))
+    return fail(FLASHMAP_E_INVALID, "num_free and max_tokens must be >= 0, with free_pages and slots when positive");
+  if (bs <= 0 || page_size <= 0 || table_rows <= 0 || req_to_page_stride <= 0 || num_pages <= 0)
+    return fail(FLASHMAP_E_INVALID, "every size must be positive");
+  if (bs > fm::kExtendMaxRequests || table_rows > fm::kExtendMaxRows)
+    return fail(FLASHMAP_E_UNSUPPORTED, "bs must be <= 8192 and table_rows <= 32768");
+  if (free_head_out == free_head || (held && held_out == held))
+    return fail(FLASHMAP_E_INVALID, "free_head_out and held_out must be other buffers than free_head and held");
+  Launch L{};
+  if (const flashmap_status st = current_launch(stream, dev_err, &L)) return st;
+  fm::ExtendPagesArgs a;
+  a.bs = bs, a.P = page_size, a.rows = table_rows, a.stride = req_to_page_stride;
+  a.req_pool_idx = req_pool_idx, a.lens = lens, a.new_lens = new_lens, a.held = held;
+  a.req_to_page = req_to_page, a.free_pages = free_pages, a.num_free = num_free;
+  a.free_head = free_head, a.free_head_out = free_head_out, a.held_out = held_out;
+  a.num_pages = num_pages, a.max_tokens = max_tokens;
+  a.cu_tokens = cu_tokens, a.slots = slots, a.positions = positions, a.token_req = token_req;
+  a.dev_err = dev_err;
+  FM_CUDA(fm::extend_pages(L, a));
+  return FLASHMAP_OK;
+}
+
+flashmap_status flashmap_tree_attention_workspace(const flashmap_cache_layer* cache, int32_t bs, int32_t width,
+                                                  int32_t num_heads, size_t* bytes) {
+  g_last_error.clear();
+  if (!bytes) return fail(FLASHMAP_E_INVALID, "NULL argument");
+  if (const flashmap_status st = check_cache_layer(cache, bs, width, num_heads)) return st;
+  Launch L{};
+  if (const flashmap_status st = current_launch(nullptr, nullptr, &L)) return st;
+  *bytes = fm::tree_attention_bytes(cache->dtype, cache->head_dim, width, num_heads / cache->num_kv_heads, L.num_sms);
+  return FLASHMAP_OK;
+}
+
+flashmap_status flashmap_tree_attention(const flashmap_cache_layer* cache, const void* q, int64_t q_stride,
+                                        int32_t bs, int32_t width, int32_t num_heads, const int32_t* ctx_lens,
+                                        const int32_t* num_nodes, const int64_t* tree_ids,
+                                        const int32_t* req_pool_idx, const int32_t* req_to_page, int32_t table_rows,
+                                        int32_t req_to_page_stride, float scale, void* out, void* workspace,
+                                        size_t workspace_bytes, uint32_t* dev_err, flashmap_stream stream) {
+  g_last_error.clear();
+  if (const flashmap_status st = check_cache_layer(cache, bs, width, num_heads)) return st;
+  if (!cache->keys || !cache->values || !q || !ctx_lens || !req_pool_idx || !req_to_page || !out)
+    return fail(FLASHMAP_E_INVALID, "NULL argument");
+  if (table_rows <= 0 || req_to_page_stride <= 0) return fail(FLASHMAP_E_INVALID, "the page table must not be empty");
+  if (!aligned16(cache->keys) || !aligned16(cache->values) || !aligned16(q) || !aligned16(out))
+    return fail(FLASHMAP_E_INVALID, "keys, values, q and out must be 16-byte aligned");
+  if (q_stride < static_cast<int64_t>(num_heads) * cache->head_dim || (q_stride * dt_size(cache->dtype)) % 16)
+    return fail(FLASHMAP_E_INVALID, "q_stride must be at least num_heads * head_dim and a multiple of 16 bytes");
+  if (!std::isfinite(scale)) return fail(FLASHMAP_E_INVALID, "scale must be finite");
+  Launch L{};
+  if (const flashmap_status st = current_launch(stream, dev_err, &L)) return st;
+  const int group = num_heads / cache->num_kv_heads;
+  const size_t need = fm::tree_attention_bytes(cache->dtype, cache->head_dim, width, group, L.num_sms);
+  if (!workspace || workspace_bytes < need)
+    return fail(FLASHMAP_E_INVALID, "workspace too small: need " + std::to_string(need) + " bytes");
+  if (!aligned16(workspace)) return fail(FLASHMAP_E_INVALID, "workspace must be 16-byte aligned");
+  fm::TreeAttnArgs a;
+  a.keys = cache->keys, a.values = cache->values, a.num_pages = cache->num_pages;
+  a.nkv = cache->num_kv_heads, a.hd = cache->head_dim, a.P = cache->page_size, a.dtype = cache->dtype;
+  a.q = q, a.q_stride = q_stride, a.bs = bs, a.width = width, a.nq = num_heads, a.group = group;
+  a.ctx_lens = ctx_lens, a.num_nodes = num_nodes, a.tree_ids = tree_ids;
+  a.req_pool_idx = req_pool_idx, a.req_to_page = req_to_page, a.table_rows = table_rows;
+  a.stride = req_to_page_stride, a.scale = scale, a.out = out, a.dev_err = dev_err;
+  FM_CUDA(fm::tree_attention(L, a, workspace));
+  return FLASHMAP_OK;
+}
+
+flashmap_status flashmap_sample_filtered(const void* logits, int32_t dtype, int32_t rows, int32_t vocab, int64_t ld,
+                                         int32_t rows_per_request, const float* temperature, const int32_t* top_k,
+                                         const float* top_p, const float* min_p, const float* uniforms,
+                                         const int64_t* ids, int64_t* tokens_out, float* probs_out,
+                                         flashmap_stream stream) {
+  g_last_error.clear();
+  if (!logits || !temperature || !uniforms || !tokens_out) return fail(FLASHMAP_E_INVALID, "NULL argument");
+  if (!is_act(dtype)) return fail(FLASHMAP_E_INVALID, "logits must be F32 or BF16");
+  if (rows <= 0 || vocab <= 0 || rows_per_request <= 0) return fail(FLASHMAP_E_INVALID, "every size must be positive");
+  if (ld < vocab) return fail(FLASHMAP_E_INVALID, "ld must be at least vocab");
+  if (vocab > fm::kSampleFilteredMaxVocab) return fail(FLASHMAP_E_UNSUPPORTED, "vocab must be <= 393216");
+  if (reinterpret_cast<uintptr_t>(logits) % dt_size(dtype)) return fail(FLASHMAP_E_INVALID, "logits are misaligned");
+  Launch L{};
+  if (const flashmap_status st = current_launch(stream, nullptr, &L)) return st;
+  fm::SampleFilteredArgs a;
+  a.logits = logits, a.dtype = dtype, a.rows = rows, a.V = vocab, a.per = rows_per_request, a.ld = ld;
+  a.temperature = temperature, a.top_k = top_k, a.top_p = top_p, a.min_p = min_p;
+  a.uniforms = uniforms, a.ids = ids, a.tokens = tokens_out, a.probs = probs_out;
+  FM_CUDA(fm::sample_filtered(L, a));
+  return FLASHMAP_OK;
+}
+
 flashmap_status flashmap_debug_philox(const uint64_t* seeds, const uint32_t* ctr, int64_t n, uint32_t* out,
                                       float* normals, flashmap_stream stream) {
   g_last_error.clear();

@@ -257,6 +257,64 @@ cudaError_t build_tree(const Launch& L, const int64_t* candidates, int bs, int N
 cudaError_t full_scatter(const Launch& L, const float* logits, int rows, int Vd, const int32_t* inv, int V,
                          float* full);
 
+// ------------------------------------------------------------------ pages.cu
+struct ExtendPagesArgs {
+  int bs = 0, P = 0, rows = 0, stride = 0;  // requests, positions per page, the table's rows and row stride
+  const int32_t *req_pool_idx = nullptr, *lens = nullptr, *new_lens = nullptr;
+  const int32_t* held = nullptr;  // pages each request's row holds, or null: ceil(lens / P)
+  int32_t* req_to_page = nullptr;
+  const int32_t* free_pages = nullptr;
+  int num_free = 0;
+  const int32_t* free_head = nullptr;
+  int32_t *free_head_out = nullptr, *held_out = nullptr;
+  int64_t num_pages = 0;
+  int max_tokens = 0;
+  int32_t* cu_tokens = nullptr;
+  int64_t* slots = nullptr;
+  int32_t *positions = nullptr, *token_req = nullptr;
+  unsigned* dev_err = nullptr;
+};
+constexpr int kExtendMaxRequests = 8192, kExtendMaxRows = 32768;  // the batch sums' shared memory
+cudaError_t extend_pages(const Launch& L, const ExtendPagesArgs& a);
+
+// ------------------------------------------------------------------ sample_filtered.cu
+struct SampleFilteredArgs {
+  const void* logits = nullptr;
+  int dtype = 0, rows = 0, V = 0, per = 1;  // row r belongs to request r / per
+  int64_t ld = 0;
+  const float* temperature = nullptr;
+  const int32_t* top_k = nullptr;   // null: off
+  const float *top_p = nullptr, *min_p = nullptr;
+  const float* uniforms = nullptr;
+  const int64_t* ids = nullptr;     // token of each vocabulary entry, or null: itself
+  int64_t* tokens = nullptr;
+  float* probs = nullptr;           // may be null
+};
+constexpr int kSampleFilteredMaxVocab = 393216;
+cudaError_t sample_filtered(const Launch& L, const SampleFilteredArgs& a);
+
+// ------------------------------------------------------------------ tree_attention.cu
+struct TreeAttnArgs {
+  const void *keys = nullptr, *values = nullptr;  // [num_pages][nkv][P][hd]
+  int64_t num_pages = 0;
+  int nkv = 0, hd = 0, P = 0, dtype = 0;
+  const void* q = nullptr;  // row b * width + i at q + (b * width + i) * q_stride, [nq][hd]
+  int64_t q_stride = 0;
+  int bs = 0, width = 0, nq = 0, group = 0;  // group = nq / nkv
+  const int32_t *ctx_lens = nullptr, *num_nodes = nullptr;  // num_nodes null: width
+  const int64_t* tree_ids = nullptr;                        // null: a chain
+  const int32_t *req_pool_idx = nullptr, *req_to_page = nullptr;
+  int table_rows = 0, stride = 0;
+  float scale = 0.f;
+  void* out = nullptr;      // [bs * width][nq][hd]
+  float* part_o = nullptr;  // two partial outputs per CTA, [2 * ctas][rows][hd], and their (max, sum)
+  float2* part_ml = nullptr;
+  unsigned* dev_err = nullptr;
+};
+// Workspace bytes of a call, and the call (false: no kernel for this shape and dtype).
+size_t tree_attention_bytes(int dtype, int hd, int width, int group, int num_sms);
+cudaError_t tree_attention(const Launch& L, TreeAttnArgs a, void* workspace);
+
 // ------------------------------------------------------------------ loadtime.cu
 struct TimeCondArgs {
   const void *te_l1_w, *te_l1_b, *te_l2_w, *te_l2_b, *je_l1_w, *je_l1_b, *je_l2_w, *je_l2_b;

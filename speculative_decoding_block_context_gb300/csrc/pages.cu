@@ -1,0 +1,187 @@
+// Page tables and slot maps from request lengths: each request's row of the page table
+// grows by the pages its new tokens need, taken from a list of free pages, and every new
+// token gets its position and its slot page * P + position % P.
+//
+// Request b holds held[b] pages and lens[b] positions and gets new_lens[b] tokens:
+//   need[b]  = max(0, ceil((lens[b] + new_lens[b]) / P) - held[b])
+//   first[b] = free_head + sum of need over the requests before b
+//   column held[b] + i of its row = free_pages[first[b] + i]
+// and its tokens are rows cu[b] .. cu[b + 1] of the outputs, cu the prefix sum of new_lens.
+//
+// One launch. What a token needs of the other requests is two prefix sums over the batch,
+// so every CTA makes both sums itself (a few integers per request, from L2, scanned in
+// shared memory) rather than wait for another CTA's: no CTA reads what another one writes
+// (old columns are read from the table, new ones from the free list).
+
+#include <algorithm>
+#include <climits>
+#include <cstdint>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace fm {
+namespace {
+
+constexpr int kPagesThreads = 512;
+constexpr int kPagesWarps = kPagesThreads / 32;
+
+// Inclusive sum over the block's threads in order, and the block's total.
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* warp_sums, int64_t& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  __syncthreads();  // the last round's readers are done with warp_sums
+  if (lane == 31) warp_sums[warp] = v;
+  __syncthreads();
+  int64_t before = 0;
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < kPagesWarps; ++w) {
+    const int64_t s = warp_sums[w];
+    if (w < warp) before += s;
+    total += s;
+  }
+  return v + before;
+}
+
+// Dynamic shared memory: cu [bs + 1], first [bs] (the request's first new page's place in
+// the free list less its held pages; kUnserved when it gets nothing), owner [table rows].
+constexpr int kUnserved = INT_MIN;
+
+__global__ void __launch_bounds__(kPagesThreads) extend_pages_kernel(const ExtendPagesArgs a) {
+  extern __shared__ int smem_pages[];
+  __shared__ int64_t warp_sums[kPagesWarps];
+  int* cu = smem_pages;
+  int* first = cu + a.bs + 1;
+  int* owner = first + a.bs;
+  pdl_trigger();
+  pdl_wait();
+  const int t = threadIdx.x;
+  const int64_t P = a.P;
+  for (int i = t; i < a.rows; i += kPagesThreads) owner[i] = INT_MAX;
+  if (t == 0) cu[0] = 0;
+  __syncthreads();
+  // a table row belongs to the first request of the batch that names it
+  for (int b = t; b < a.bs; b += kPagesThreads) {
+    const int r = LDCG(a.req_pool_idx + b);
+    if (r >= 0 && r < a.rows) atomicMin(owner + r, b);
+  }
+  __syncthreads();
+  const int head = LDCG(a.free_head);
+  const bool head_ok = head >= 0 && head <= a.num_free;
+  unsigned err = head_ok ? 0u : FLASHMAP_DEVERR_CAPACITY;
+  int64_t tokens = 0, pages = 0;  // of the requests before this chunk
+  int64_t taken = 0;              // pages handed out
+  for (int b0 = 0; b0 < a.bs; b0 += kPagesThreads) {
+    const int b = b0 + t;
+    int64_t len = 0, add = 0, held = 0, end = 0;
+    bool ok = false;
+    if (b < a.bs) {
+      const int r = LDCG(a.req_pool_idx + b);
+      len = LDCG(a.lens + b);
+      add = LDCG(a.new_lens + b);
+      held = a.held ? LDCG(a.held + b) : (len + P - 1) / P;
+      ok = true;
+      if (add < 0 || len < 0 || len + add > INT_MAX) {
+        err |= FLASHMAP_DEVERR_POSITION;
+        ok = false;
+        add = max(add, static_cast<int64_t>(0));
+      }
+      if (r < 0 || r >= a.rows || owner[r] != b || held * P < len) {
+        err |= FLASHMAP_DEVERR_REQUEST;
+        ok = false;
+      }
+      end = (len + add + P - 1) / P;
+      if (ok && max(end, held) > a.stride) {
+        err |= FLASHMAP_DEVERR_POSITION;
+        ok = false;
+      }
+    }
+    int64_t chunk;
+    const int64_t upto = tokens + block_scan(add, warp_sums, chunk);  // rows up to this request's end
+    tokens += chunk;
+    if (b < a.bs && ok && add > 0 && upto > a.max_tokens) {
+      err |= FLASHMAP_DEVERR_CAPACITY;
+      ok = false;
+    }
+    const int64_t need = ok ? max(end - held, static_cast<int64_t>(0)) : 0;
+    const int64_t last = pages + block_scan(need, warp_sums, chunk);  // its pages' end, from the head
+    pages += chunk;
+    if (need > 0 && (!head_ok || head + last > a.num_free)) {
+      err |= FLASHMAP_DEVERR_CAPACITY;
+      ok = false;
+    }
+    if (b < a.bs) {
+      cu[b + 1] = static_cast<int>(min(upto, static_cast<int64_t>(INT_MAX)));
+      first[b] = ok ? static_cast<int>(head + last - need - held) : kUnserved;
+      if (ok) taken = max(taken, need > 0 ? last : static_cast<int64_t>(0));
+      if (blockIdx.x == 0 && a.held_out)
+        a.held_out[b] = static_cast<int>(held + (ok ? need : 0));
+    }
+  }
+  __syncthreads();
+  if (blockIdx.x == 0) {
+    for (int b = t; b <= a.bs; b += kPagesThreads) a.cu_tokens[b] = cu[b];
+    // pages handed out: the requests served take a contiguous run of the list
+    for (int o = 16; o > 0; o >>= 1) taken = max(taken, __shfl_xor_sync(0xffffffffu, taken, o));
+    if ((t & 31) == 0) warp_sums[t >> 5] = taken;
+    __syncthreads();
+    if (t == 0) {
+      for (int w = 1; w < kPagesWarps; ++w) taken = max(taken, warp_sums[w]);
+      *a.free_head_out = static_cast<int>(head + taken);
+    }
+  }
+  const int rows = static_cast<int>(min(tokens, static_cast<int64_t>(a.max_tokens)));
+  for (int64_t j64 = static_cast<int64_t>(blockIdx.x) * kPagesThreads + t; j64 < rows;
+       j64 += static_cast<int64_t>(gridDim.x) * kPagesThreads) {
+    const int j = static_cast<int>(j64);
+    int lo = 0, hi = a.bs - 1;  // the request: the last b with cu[b] <= j (empty ones hold no row)
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (cu[mid] <= j) lo = mid; else hi = mid - 1;
+    }
+    const int b = lo;
+    const int64_t pos = static_cast<int64_t>(LDCG(a.lens + b)) + (j - cu[b]);
+    int64_t slot = -1;
+    const int f = first[b];
+    if (f != kUnserved) {
+      const unsigned up = static_cast<unsigned>(pos), uP = static_cast<unsigned>(a.P);
+      const unsigned col = up / uP, off = up - col * uP;
+      const int64_t row = static_cast<int64_t>(LDCG(a.req_pool_idx + b)) * a.stride;
+      const int held = a.held ? LDCG(a.held + b)
+                              : static_cast<int>((static_cast<unsigned>(LDCG(a.lens + b)) + uP - 1) / uP);
+      const bool fresh = static_cast<int>(col) >= held;
+      const int page = fresh ? LDCG(a.free_pages + (f + static_cast<int64_t>(col))) : LDCG(a.req_to_page + row + col);
+      if (page < 0 || page >= a.num_pages) {
+        err |= FLASHMAP_DEVERR_PAGE;
+      } else {
+        slot = static_cast<int64_t>(page) * a.P + off;
+        if (fresh && off == 0) a.req_to_page[row + col] = page;
+      }
+    }
+    a.slots[j] = slot;
+    if (a.positions) a.positions[j] = static_cast<int>(pos);
+    if (a.token_req) a.token_req[j] = b;
+  }
+  if (err) set_dev_error(a.dev_err, err);
+}
+
+}  // namespace
+
+cudaError_t extend_pages(const Launch& L, const ExtendPagesArgs& a) {
+  const size_t smem = sizeof(int) * (2 * static_cast<size_t>(a.bs) + 1 + a.rows);
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(extend_pages_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+  }
+  const int64_t tiles = (static_cast<int64_t>(a.max_tokens) + kPagesThreads - 1) / kPagesThreads;
+  const int grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(tiles, L.num_sms)));
+  return launch_k(L, extend_pages_kernel, dim3(grid), dim3(kPagesThreads), smem, a);
+}
+
+}  // namespace fm
