@@ -15,7 +15,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(HERE, "libflashmap.so")
 SOURCES = ["gemm.cu", "attention.cu", "rows.cu", "sample.cu", "tree.cu", "pages.cu",
-           "tree_attention.cu", "sample_filtered.cu", "jumps.cu", "eigen.cu", "loadtime.cu", "flashmap.cu"]
+           "tree_attention.cu", "tree_mma.cu", "sample_filtered.cu", "jumps.cu", "eigen.cu", "loadtime.cu", "flashmap.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "-I", CSRC, "-I", INCLUDE] + ARCH
 

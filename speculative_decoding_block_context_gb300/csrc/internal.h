@@ -311,9 +311,13 @@ struct TreeAttnArgs {
   float2* part_ml = nullptr;
   unsigned* dev_err = nullptr;
 };
-// Workspace bytes of a call, and the call (false: no kernel for this shape and dtype).
+// Workspace bytes of a call, and the call.
 size_t tree_attention_bytes(int dtype, int hd, int width, int group, int num_sms);
 cudaError_t tree_attention(const Launch& L, TreeAttnArgs a, void* workspace);
+// The tensor-core kernel (tree_mma.cu): bf16 heads of 64 and 128.
+inline bool tree_mma_fits(int dtype, int hd) { return dtype == FLASHMAP_BF16 && (hd == 64 || hd == 128); }
+size_t tree_mma_bytes(int hd, int width, int group, int num_sms);
+cudaError_t tree_mma(const Launch& L, TreeAttnArgs a, void* workspace);
 
 // ------------------------------------------------------------------ loadtime.cu
 struct TimeCondArgs {
