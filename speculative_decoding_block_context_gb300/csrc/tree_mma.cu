@@ -208,10 +208,14 @@ __global__ void __launch_bounds__(MmaCfg<HD, MT>::THREADS, 1)
         if (lane == 0) blocks_ok[seq & 15] = static_cast<uint8_t>(bits);
         ++seq;
         if (!(ok = load_tile(&kmap, row))) break;
-        if (t > w.t0 && !(ok = load_tile(&vmap, row_prev))) break;
+        if (NB == 1) {
+          if (!(ok = load_tile(&vmap, row))) break;
+        } else if (t > w.t0 && !(ok = load_tile(&vmap, row_prev))) {
+          break;
+        }
         row_prev = row;
       }
-      if (ok) ok = load_tile(&vmap, row_prev);
+      if (ok && NB == 2) ok = load_tile(&vmap, row_prev);
     }
     if (lane == 0) s_issued = issued;
   } else if (warp == 1) {
@@ -244,59 +248,82 @@ __global__ void __launch_bounds__(MmaCfg<HD, MT>::THREADS, 1)
         ++ns[m];
         return true;
       };
-      auto next_slot = [&]() {
+      auto release_slot = [&]() {
         if (lane == 0) umma_commit(&empty[slot]);  // free once the products issued so far are done
         if (++slot == SLOTS) slot = 0, phase ^= 1u;
       };
+      // the values of tile t are in the slot: nothing past the request's end may reach a sum
+      auto clear_tail = [&](int t, int at) {
+        const int left = end - t * TN;  // positions of the tile that exist
+        if (left >= TN || !(left & 15)) return;
+        // the last block's rows past the end hold whatever the page held: their weights
+        // are 0, but 0 times a NaN is not
+        const int r1 = (left + 15) & ~15;
+        uint8_t* base = ring + at * C::TILE;
+        for (int x = lane; x < (r1 - left) * 8 * (HD / 64); x += 32) {
+          const int h = x / ((r1 - left) * 8), y = x - h * (r1 - left) * 8;
+          *reinterpret_cast<uint4*>(base + h * HALF + left * 128 + y * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_async_smem();
+        __syncwarp();
+      };
+      auto weighted_sum = [&](int t, int m, uint32_t vaddr) {
+        const int buf = np[m] % NB;
+        if (!warp_wait(&p_ready[m][buf], (np[m] / NB) & 1, ab)) return false;
+        // the item before has read its output
+        if (t == w.t0 && items[m] > 0 && !warp_wait(&o_free[m], (items[m] - 1) & 1, ab)) return false;
+        tc_fence_after();
+        if (lane == 0) {
+          const uint32_t d = tmem + C::O_COL + static_cast<uint32_t>(m * 128);
+          const uint32_t p = tmem + static_cast<uint32_t>((m * NB + buf) * 128);
+#pragma unroll
+          for (int s = 0; s < TN / 16; ++s)
+            umma_bf16_ts(d, p + 8 * s, sdesc_sw128_rows_k(vaddr + s * 2048, HALF), idesc_o, t > w.t0 || s > 0);
+          umma_commit(&pv_done[m][buf]);
+        }
+        ++np[m];
+        if (t == w.t1 - 1) ++items[m];
+        return true;
+      };
+      // Step t: the scores of tile t and the values of tile t - 1. With two S buffers the
+      // scores go first (they run while the softmax of tile t - 1 does); with one they
+      // follow the product that takes P out of it.
       for (int t = w.t0; ok && t <= w.t1; ++t) {
-        if (t < w.t1) {
-          if (!(ok = warp_wait(&full[slot], phase, ab))) break;
-          tc_fence_after();
+        const bool has_s = t < w.t1, has_v = t > w.t0;
+        if constexpr (NB == 2) {
+          if (has_s) {
+            if (!(ok = warp_wait(&full[slot], phase, ab))) break;
+            if (t == w.t0 && !(ok = warp_wait(&q_ready[0], items[0] & 1, ab))) break;
+            if (!(ok = scores(0, r0 + slot * C::TILE))) break;
+            __syncwarp();
+            release_slot();
+          }
+          if (has_v) {
+            if (!(ok = warp_wait(&full[slot], phase, ab))) break;
+            clear_tail(t - 1, slot);
+            if (!(ok = weighted_sum(t - 1, 0, r0 + slot * C::TILE))) break;
+            __syncwarp();
+            release_slot();
+          }
+        } else {
+          const int vs = slot, ks = !has_v ? slot : slot + 1 == SLOTS ? 0 : slot + 1;
+          const uint32_t k_phase = ks < vs ? phase ^ 1u : phase;
+          if (has_v) {
+            if (!(ok = warp_wait(&full[vs], phase, ab))) break;
+            clear_tail(t - 1, vs);
+          }
           for (int m = 0; ok && m < nm; ++m) {
-            if (t == w.t0) ok = warp_wait(&q_ready[m], items[m] & 1, ab);
-            if (ok) ok = scores(m, r0 + slot * C::TILE);
+            if (has_v && !(ok = weighted_sum(t - 1, m, r0 + vs * C::TILE))) break;
+            if (!has_s) continue;
+            if (m == 0 && !(ok = warp_wait(&full[ks], k_phase, ab))) break;
+            if (t == w.t0 && !(ok = warp_wait(&q_ready[m], items[m] & 1, ab))) break;
+            ok = scores(m, r0 + ks * C::TILE);
           }
           if (!ok) break;
           __syncwarp();
-          next_slot();
+          if (has_v) release_slot();
+          if (has_s) release_slot();
         }
-        if (t == w.t0) continue;
-        // the values of tile t - 1
-        if (!(ok = warp_wait(&full[slot], phase, ab))) break;
-        const int left = end - (t - 1) * TN;  // positions of the tile that exist
-        if (left < TN && (left & 15)) {
-          // the last block's rows past the end hold whatever the page held: their weights
-          // are 0, and 0 times a NaN must not reach the sum
-          const int r1 = (left + 15) & ~15;
-          uint8_t* base = ring + slot * C::TILE;
-          for (int x = lane; x < (r1 - left) * 8 * (HD / 64); x += 32) {
-            const int h = x / ((r1 - left) * 8), y = x - h * (r1 - left) * 8;
-            *reinterpret_cast<uint4*>(base + h * HALF + left * 128 + y * 16) = make_uint4(0, 0, 0, 0);
-          }
-          fence_async_smem();
-          __syncwarp();
-        }
-        for (int m = 0; ok && m < nm; ++m) {
-          const int buf = np[m] % NB;
-          if (!(ok = warp_wait(&p_ready[m][buf], (np[m] / NB) & 1, ab))) break;
-          // the item before has read its output
-          if (t - 1 == w.t0 && items[m] > 0 && !(ok = warp_wait(&o_free[m], (items[m] - 1) & 1, ab))) break;
-          tc_fence_after();
-          if (lane == 0) {
-            const uint32_t d = tmem + C::O_COL + static_cast<uint32_t>(m * 128);
-            const uint32_t p = tmem + static_cast<uint32_t>((m * NB + buf) * 128);
-            const uint32_t v = r0 + slot * C::TILE;
-#pragma unroll
-            for (int s = 0; s < TN / 16; ++s)
-              umma_bf16_ts(d, p + 8 * s, sdesc_sw128_rows_k(v + s * 2048, HALF), idesc_o, t - 1 > w.t0 || s > 0);
-            umma_commit(&pv_done[m][buf]);
-          }
-          ++np[m];
-          if (t == w.t1) ++items[m];
-        }
-        if (!ok) break;
-        __syncwarp();
-        next_slot();
       }
     }
     // nothing of this CTA may be in flight when its TMEM is freed

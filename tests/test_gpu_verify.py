@@ -203,6 +203,8 @@ SHAPES = [
     (2, 130, 7, 1, 64, 128, [5, 260], None, False),       # many row tiles, a group of 7
     (1, 300, 2, 1, 128, 16, [40], None, True),            # a tree wider than a position tile
     (1, 4, 4, 1, 128, 16, [9000], None, True),            # one row tile over many CTAs
+    (3, 64, 32, 8, 128, 16, [5000, 9000, 300], [64, 64, 20], True),  # two row tiles over many positions
+    (3, 50, 24, 4, 64, 32, [6000, 4001, 9000], [50, 3, 27], False),
     (40, 2, 4, 2, 64, 16, [3 * i for i in range(40)], None, True),
 ]
 
