@@ -475,6 +475,8 @@ flashmap_status flashmap_tree_attention_workspace(const flashmap_cache_layer* ca
  *                width 1: single tokens)
  *   req_pool_idx (device) int32 [bs]; req_to_page (device) int32 [table_rows][stride]
  *   out          (device, 16-byte aligned) [bs * width][num_heads][head_dim]
+ *   workspace    (device, 256-byte aligned) flashmap_tree_attention_workspace bytes; its
+ *                contents do not matter, one call at a time may use it
  * Scores, the softmax and its sums are float32; with BF16 the probabilities are rounded to
  * bf16 for their product with the values. Cached keys and values of visible positions must
  * be finite or give NaN; positions past a request's last node are not read into results.

@@ -180,6 +180,16 @@ def _stream(stream):
     return _vp(torch.cuda.current_stream().cuda_stream)
 
 
+def _here(stream, t):
+    """The stream handle as an integer, the one given or torch's current one; t must be on the current device."""
+    import torch
+
+    device = torch._C._cuda_getDevice()
+    if t.get_device() != device:
+        raise ValueError(f"the tensors are on {t.device}, the current device is cuda:{device}")
+    return stream if stream is not None else torch._C._cuda_getCurrentRawStream(device)
+
+
 def make_config(d: dict) -> flashmap_config:
     c = flashmap_config()
     for name, ctype in flashmap_config._fields_:
@@ -315,13 +325,28 @@ def flashmap_build_tree(candidates, width: int, tokens_out, ids_out, stats_out, 
                                      _ptr(ids_out), _ptr(stats_out), _stream(stream)))
 
 
-def _dense(name: str, t, dtype: str, n: int | None = None):
-    """Checks that t is a contiguous CUDA tensor of this dtype (and of n elements at least); its pointer."""
+_DT = {}  # torch dtypes by short name, filled once
+
+
+def _dtypes() -> dict:
+    if not _DT:
+        import torch
+
+        _DT.update(i32=torch.int32, i64=torch.int64, f32=torch.float32, bf16=torch.bfloat16)
+    return _DT
+
+
+def _bad(name: str, t, dtype, n: int):
+    raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor of at least {n} elements, got "
+                     f"{tuple(t.shape)} {t.dtype} on {t.device}")
+
+
+def _dense(name: str, t, dtype, n: int = 0):
+    """The pointer of t (None for None), checked: contiguous, on the GPU, this dtype, n elements at least."""
     if t is None:
         return None
-    if not t.is_cuda or str(t.dtype)[6:] != dtype or not t.is_contiguous() or (n is not None and t.numel() < n):
-        raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor" +
-                         (f" of at least {n} elements" if n is not None else ""))
+    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous() or t.numel() < n:
+        _bad(name, t, dtype, n)
     return t.data_ptr()
 
 
@@ -329,29 +354,32 @@ def flashmap_extend_pages(req_pool_idx, lens, new_lens, held, page_size: int, re
                           free_head_out, held_out, num_pages: int, cu_tokens, slots, positions=None, token_req=None,
                           dev_err=None, stream=None) -> None:
     """Extends req_to_page (rows, stride) in place; slots' length is the most tokens a call may have."""
+    dt = _dtypes()
+    i32, i64 = dt["i32"], dt["i64"]
     bs, most = req_pool_idx.numel(), slots.numel()
     if req_to_page.dim() != 2:
         raise ValueError("req_to_page must be (rows, stride)")
     rows, stride = req_to_page.shape
     _check(lib().flashmap_extend_pages(
-        bs, _dense("req_pool_idx", req_pool_idx, "int32"), _dense("lens", lens, "int32", bs),
-        _dense("new_lens", new_lens, "int32", bs), _dense("held", held, "int32", bs), page_size,
-        _dense("req_to_page", req_to_page, "int32"), rows, stride, _dense("free_pages", free_pages, "int32"),
-        free_pages.numel(), _dense("free_head", free_head, "int32", 1),
-        _dense("free_head_out", free_head_out, "int32", 1), _dense("held_out", held_out, "int32", bs), num_pages, most,
-        _dense("cu_tokens", cu_tokens, "int32", bs + 1), _dense("slots", slots, "int64"),
-        _dense("positions", positions, "int32", most), _dense("token_req", token_req, "int32", most),
-        _dense("dev_err", dev_err, "int32", 1), _stream(stream)))
+        bs, _dense("req_pool_idx", req_pool_idx, i32), _dense("lens", lens, i32, bs),
+        _dense("new_lens", new_lens, i32, bs), _dense("held", held, i32, bs), page_size,
+        _dense("req_to_page", req_to_page, i32), rows, stride, _dense("free_pages", free_pages, i32),
+        free_pages.numel(), _dense("free_head", free_head, i32, 1),
+        _dense("free_head_out", free_head_out, i32, 1), _dense("held_out", held_out, i32, bs), num_pages, most,
+        _dense("cu_tokens", cu_tokens, i32, bs + 1), _dense("slots", slots, i64),
+        _dense("positions", positions, i32, most), _dense("token_req", token_req, i32, most),
+        _dense("dev_err", dev_err, i32, 1), _here(stream, slots)))
 
 
 def make_cache_layer(keys, values) -> flashmap_cache_layer:
     """One layer's paged keys and values, each (num_pages, num_kv_heads, page_size, head_dim)."""
-    kind = str(keys.dtype)[6:]
-    if keys.dim() != 4 or keys.shape != values.shape or kind not in ("float32", "bfloat16"):
+    f32, bf16 = _dtypes()["f32"], _dtypes()["bf16"]
+    kind = keys.dtype
+    if keys.dim() != 4 or keys.shape != values.shape or kind not in (f32, bf16):
         raise ValueError("keys and values must be float32 or bfloat16 (num_pages, num_kv_heads, page_size, head_dim)")
     pages, heads, page, hd = keys.shape
     c = flashmap_cache_layer(_dense("keys", keys, kind), _dense("values", values, kind), pages, heads, page, hd,
-                             F32 if kind == "float32" else BF16)
+                             F32 if kind is f32 else BF16)
     c.kind, c._keep = kind, (keys, values)
     return c
 
@@ -366,39 +394,46 @@ def flashmap_tree_attention(cache: flashmap_cache_layer, q, width: int, ctx_lens
                             req_to_page, scale: float, out, workspace, dev_err=None, stream=None) -> None:
     """q (bs * width, num_heads, head_dim), its rows possibly further apart (a slice of a wider
     projection); out the same shape, contiguous; tree_ids (bs, width - 1) from flashmap_build_tree or None."""
-    bs, heads, hd = ctx_lens.numel(), q.shape[1], q.shape[2]
-    if not q.is_cuda or str(q.dtype)[6:] != cache.kind or q.shape[0] != bs * width or hd != cache.head_dim or \
-            q.stride(2) != 1 or q.stride(1) != hd:
+    dt = _dtypes()
+    i32, i64 = dt["i32"], dt["i64"]
+    bs = ctx_lens.numel()
+    n, heads, hd = q.shape
+    step, head_step, one = q.stride()
+    if q.dtype is not cache.kind or not q.is_cuda or n != bs * width or hd != cache.head_dim or one != 1 or \
+            (head_step != hd and heads > 1):
         raise ValueError("q must be (bs * width, num_heads, head_dim) in the cache's dtype with dense rows")
     if req_to_page.dim() != 2:
         raise ValueError("req_to_page must be (rows, stride)")
     rows, stride = req_to_page.shape
     _check(lib().flashmap_tree_attention(
-        _c.byref(cache), q.data_ptr(), q.stride(0) if bs * width > 1 else heads * hd, bs, width, heads,
-        _dense("ctx_lens", ctx_lens, "int32"), _dense("num_nodes", num_nodes, "int32", bs),
-        _dense("tree_ids", tree_ids, "int64", bs * (width - 1)), _dense("req_pool_idx", req_pool_idx, "int32", bs),
-        _dense("req_to_page", req_to_page, "int32"), rows, stride, scale,
+        _c.byref(cache), q.data_ptr(), step if n > 1 else heads * hd, bs, width, heads,
+        _dense("ctx_lens", ctx_lens, i32), _dense("num_nodes", num_nodes, i32, bs),
+        _dense("tree_ids", tree_ids, i64, bs * (width - 1)), _dense("req_pool_idx", req_pool_idx, i32, bs),
+        _dense("req_to_page", req_to_page, i32), rows, stride, scale,
         _dense("out", out, cache.kind, bs * width * heads * hd), workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _dense("dev_err", dev_err, "int32", 1), _stream(stream)))
+        workspace.numel() * workspace.element_size(), _dense("dev_err", dev_err, i32, 1), _here(stream, q)))
 
 
 def flashmap_sample_filtered(logits, rows_per_request: int, temperature, top_k, top_p, min_p, uniforms, ids,
                              tokens_out, probs_out=None, stream=None) -> None:
     """logits (rows, vocab) float32 or bfloat16, rows possibly further apart than vocab; top_k, top_p,
     min_p, ids and probs_out may be None."""
-    kind = str(logits.dtype)[6:]
-    if not logits.is_cuda or logits.dim() != 2 or kind not in ("float32", "bfloat16") or logits.stride(1) != 1:
+    dt = _dtypes()
+    i32, i64, f32 = dt["i32"], dt["i64"], dt["f32"]
+    kind = logits.dtype
+    if logits.dim() != 2 or not logits.is_cuda or kind not in (f32, dt["bf16"]) or \
+            (logits.stride(1) != 1 and logits.shape[1] > 1):
         raise ValueError("logits must be a CUDA float32 or bfloat16 (rows, vocab) tensor with dense rows")
     rows, vocab = logits.shape
     bs = -(-rows // max(1, rows_per_request))
     _check(lib().flashmap_sample_filtered(
-        logits.data_ptr(), F32 if kind == "float32" else BF16, rows, vocab,
+        logits.data_ptr(), F32 if kind is f32 else BF16, rows, vocab,
         logits.stride(0) if rows > 1 else vocab,
-        rows_per_request, _dense("temperature", temperature, "float32", bs), _dense("top_k", top_k, "int32", bs),
-        _dense("top_p", top_p, "float32", bs), _dense("min_p", min_p, "float32", bs),
-        _dense("uniforms", uniforms, "float32", rows), _dense("ids", ids, "int64", vocab),
-        _dense("tokens_out", tokens_out, "int64", rows), _dense("probs_out", probs_out, "float32", rows),
-        _stream(stream)))
+        rows_per_request, _dense("temperature", temperature, f32, bs), _dense("top_k", top_k, i32, bs),
+        _dense("top_p", top_p, f32, bs), _dense("min_p", min_p, f32, bs),
+        _dense("uniforms", uniforms, f32, rows), _dense("ids", ids, i64, vocab),
+        _dense("tokens_out", tokens_out, i64, rows), _dense("probs_out", probs_out, f32, rows),
+        _here(stream, logits)))
 
 
 def flashmap_get_device_error(model: Model, stream=None) -> int:

@@ -1587,7 +1587,8 @@ flashmap_status flashmap_tree_attention(const flashmap_cache_layer* cache, const
   const size_t need = fm::tree_attention_bytes(cache->dtype, cache->head_dim, width, group, L.num_sms);
   if (!workspace || workspace_bytes < need)
     return fail(FLASHMAP_E_INVALID, "workspace too small: need " + std::to_string(need) + " bytes");
-  if (!aligned16(workspace)) return fail(FLASHMAP_E_INVALID, "workspace must be 16-byte aligned");
+  if (reinterpret_cast<uintptr_t>(workspace) & 255)
+    return fail(FLASHMAP_E_INVALID, "workspace must be 256-byte aligned");
   fm::TreeAttnArgs a;
   a.keys = cache->keys, a.values = cache->values, a.num_pages = cache->num_pages;
   a.nkv = cache->num_kv_heads, a.hd = cache->head_dim, a.P = cache->page_size, a.dtype = cache->dtype;

@@ -307,6 +307,7 @@ struct TreeAttnArgs {
   int table_rows = 0, stride = 0;
   float scale = 0.f;
   void* out = nullptr;      // [bs * width][nq][hd]
+  void* tasks = nullptr;    // what the joining kernel does per CTA (tree_common.cuh)
   float* part_o = nullptr;  // two partial outputs per CTA, [2 * ctas][rows][hd], and their (max, sum)
   float2* part_ml = nullptr;
   unsigned* dev_err = nullptr;

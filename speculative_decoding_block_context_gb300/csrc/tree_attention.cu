@@ -68,15 +68,13 @@ __global__ void __launch_bounds__(256) tree_simt_kernel(const TreeAttnArgs a) {
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   unsigned err = 0;
   Spot spot;
-  const int G = gridDim.x, c = blockIdx.x;
-  const int64_t units = locate<C::THREADS, TM, TN>(a, c, G, spot, err, red, &s_spot);
-  const int64_t u0 = units * c / G, u1 = units * (c + 1) / G;
-  Walk<TM, TN> w(a, spot, u0, u1);
+  const Share share = locate<C::THREADS, TM, TN>(a, 1, spot, err, red, &s_spot);
+  Walk<TM, TN> w(a, share, spot);
   const float k2 = a.scale * 1.4426950408889634f;
   int tree_b = -1;
   while (w.next(a)) {
     const int rows = min(TM, w.r.n * a.group - w.tile_m * TM);
-    const int64_t table = static_cast<int64_t>(LDCG(a.req_pool_idx + w.b)) * a.stride;
+    const int64_t table = static_cast<int64_t>(w.r.row) * a.stride;
     const int end = w.r.ctx + w.r.n;
     __syncthreads();
     if (w.t1 * TN > w.r.ctx && tree_b != w.b) {  // the item reaches the tree
@@ -218,7 +216,7 @@ __global__ void __launch_bounds__(256) tree_simt_kernel(const TreeAttnArgs a) {
         }
       }
     }
-    const int slot = 2 * c + (w.first_item ? 0 : 1);
+    const int slot = 2 * static_cast<int>(blockIdx.x) + (w.first_item ? 0 : 1);
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       const int row = ty + 16 * r;
@@ -240,6 +238,7 @@ __global__ void __launch_bounds__(256) tree_simt_kernel(const TreeAttnArgs a) {
       }
     }
   }
+  if (tid == 0) write_join_task(a, share, w);
   if (err) set_dev_error(a.dev_err, err);
 }
 
@@ -249,7 +248,7 @@ cudaError_t launch_simt(const Launch& L, const TreeAttnArgs& a, int G) {
   cudaError_t e = cudaFuncSetAttribute(tree_simt_kernel<T, HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e == cudaSuccess) e = launch_k(L, tree_simt_kernel<T, HD>, dim3(G), dim3(C::THREADS), C::SMEM, a);
   if (e == cudaSuccess && G > 1)
-    e = launch_k(L, tree_join_kernel<T, HD, C::TM, C::TN>, dim3(G - 1, kJoinY), dim3(kJoinThreads), 0, a);
+    e = launch_k(L, tree_join_kernel<T, HD, C::TM>, dim3(G - 1, kJoinY), dim3(kJoinThreads), 0, a);
   return e;
 }
 
@@ -268,7 +267,8 @@ cudaError_t launch_simt_hd(const Launch& L, const TreeAttnArgs& a, int G) {
 namespace {
 int simt_ctas(int num_sms) { return 2 * num_sms; }
 size_t simt_bytes(int hd, int num_sms) {
-  return static_cast<size_t>(2 * simt_ctas(num_sms)) * 32 * (static_cast<size_t>(hd) * 4 + 8);
+  return join_tasks_bytes(simt_ctas(num_sms)) +
+         static_cast<size_t>(2 * simt_ctas(num_sms)) * 32 * (static_cast<size_t>(hd) * 4 + 8);
 }
 }  // namespace
 
@@ -279,7 +279,8 @@ size_t tree_attention_bytes(int dtype, int hd, int width, int group, int num_sms
 cudaError_t tree_attention(const Launch& L, TreeAttnArgs a, void* workspace) {
   if (tree_mma_fits(a.dtype, a.hd)) return tree_mma(L, a, workspace);
   const int G = simt_ctas(L.num_sms);
-  a.part_ml = static_cast<float2*>(workspace);
+  a.tasks = workspace;
+  a.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + join_tasks_bytes(G));
   a.part_o = reinterpret_cast<float*>(a.part_ml + static_cast<size_t>(2 * G) * 32);
   return a.dtype == FLASHMAP_F32 ? launch_simt_hd<float>(L, a, G) : launch_simt<__nv_bfloat16, 32>(L, a, G);
 }

@@ -17,16 +17,17 @@ constexpr int kTreeMaxWidth = kTreeMaxNodes + 1;
 
 struct Request {
   int ctx, n;  // positions before the root, nodes (0: nothing to do)
+  int row;     // page-table row
 };
 
 __device__ __forceinline__ Request request_of(const TreeAttnArgs& a, int b, unsigned& err) {
   Request r;
   r.ctx = LDCG(a.ctx_lens + b);
   r.n = a.num_nodes ? LDCG(a.num_nodes + b) : a.width;
+  r.row = LDCG(a.req_pool_idx + b);
   if (r.n < 0 || r.n > a.width) err |= FLASHMAP_DEVERR_TREE, r.n = min(max(r.n, 0), a.width);
   if (r.ctx < 0 || r.ctx > INT_MAX - kTreeMaxWidth - 256) err |= FLASHMAP_DEVERR_POSITION, r.n = 0, r.ctx = 0;
-  const int row = LDCG(a.req_pool_idx + b);
-  if (row < 0 || row >= a.table_rows) err |= FLASHMAP_DEVERR_REQUEST, r.n = 0;
+  if (r.row < 0 || r.row >= a.table_rows) err |= FLASHMAP_DEVERR_REQUEST, r.n = 0;
   return r;
 }
 
@@ -39,9 +40,32 @@ struct Cut {
   }
 };
 
+// 64-bit quotients take hundreds of cycles and nearly all of these fit 32 bits.
+__device__ __forceinline__ int64_t quotient(int64_t x, int y) {
+  if ((x >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
+  return x / y;
+}
+
+// T units over `ctas` CTAs; CTA c takes units [begin(c), begin(c + 1)), begin(c) = floor(T c / ctas).
+struct Share {
+  int64_t T;
+  int ctas;
+  __device__ Share(int64_t units, int grid, int least) : T(units) {
+    // no CTA with fewer than `least` units (but one): shorter shares cost more in partial
+    // sums than they save
+    ctas = static_cast<int>(max(static_cast<int64_t>(1), min(static_cast<int64_t>(grid), quotient(T, least))));
+  }
+  __device__ int64_t begin(int c) const {
+    const int64_t q = quotient(T, ctas);
+    const int r = static_cast<int>(T - q * ctas);
+    return q * c + static_cast<uint32_t>(r * c) / static_cast<uint32_t>(ctas);  // r c < ctas^2
+  }
+};
+
 struct Spot {
   int b;         // the request that holds the unit
   int64_t base;  // its first unit
+  Request r;
 };
 
 // Inclusive sum over the block in thread order; `total` over all threads.
@@ -67,40 +91,46 @@ __device__ __forceinline__ int64_t unit_scan(int64_t v, int64_t* red, int64_t& t
   return v + before;
 }
 
-// The batch's units T, and the request of unit T c / G (b = bs when there is none, T = 0).
-// Called by the whole block; every thread gets the answer.
+// The batch's share out, and the request of CTA blockIdx.x's first unit (b = bs when it has
+// none). Called by the whole block; every thread gets the answer.
 template <int THREADS, int TM, int TN>
-__device__ __forceinline__ int64_t locate(const TreeAttnArgs& a, int c, int G, Spot& spot, unsigned& err,
-                                          int64_t* red, Spot* shared_spot) {
+__device__ __forceinline__ Share locate(const TreeAttnArgs& a, int least, Spot& spot, unsigned& err, int64_t* red,
+                                        Spot* shared_spot) {
   const int t = threadIdx.x;
   int64_t T = 0, mine = 0, incl = 0;
+  Request r{0, 0, 0};
   for (int b0 = 0; b0 < a.bs; b0 += THREADS) {
     const int b = b0 + t;
-    const int64_t v = b < a.bs ? Cut<TM, TN>::units(a, request_of(a, b, err)) : 0;
+    Request x{0, 0, 0};
+    if (b < a.bs) x = request_of(a, b, err);
+    const int64_t v = Cut<TM, TN>::units(a, x);
     int64_t chunk;
     const int64_t i = unit_scan<THREADS>(v, red, chunk);
-    if (b0 == 0) mine = v, incl = i;
+    if (b0 == 0) mine = v, incl = i, r = x;
     T += chunk;
   }
-  if (t == 0) *shared_spot = Spot{a.bs, 0};
+  if (t == 0) *shared_spot = Spot{a.bs, 0, {0, 0, 0}};
   __syncthreads();
-  const int64_t u = T * c / G;
-  if (t < a.bs && incl - mine <= u && u < incl) *shared_spot = Spot{t, incl - mine};
-  int64_t before = 0;
+  const Share share(T, gridDim.x, least);
+  const int64_t u = static_cast<int>(blockIdx.x) < share.ctas ? share.begin(blockIdx.x) : T;
+  if (t < a.bs && incl - mine <= u && u < incl) *shared_spot = Spot{t, incl - mine, r};
   if (a.bs > THREADS) {  // the unit may lie past the first chunk
+    int64_t before = 0;
     unsigned none = 0;
     for (int b0 = 0; b0 < a.bs; b0 += THREADS) {
       const int b = b0 + t;
-      const int64_t v = b < a.bs ? Cut<TM, TN>::units(a, request_of(a, b, none)) : 0;
+      Request x{0, 0, 0};
+      if (b < a.bs) x = request_of(a, b, none);
+      const int64_t v = Cut<TM, TN>::units(a, x);
       int64_t chunk;
       const int64_t i = before + unit_scan<THREADS>(v, red, chunk);
-      if (b0 > 0 && b < a.bs && i - v <= u && u < i) *shared_spot = Spot{b, i - v};
+      if (b0 > 0 && b < a.bs && i - v <= u && u < i) *shared_spot = Spot{b, i - v, x};
       before += chunk;
     }
   }
   __syncthreads();
   spot = *shared_spot;
-  return T;
+  return share;
 }
 
 // One CTA's walk over its units, row tile by row tile.
@@ -109,31 +139,32 @@ struct Walk {
   int64_t u, u1, base;  // next unit, the range's end, the request's first unit
   int b;
   Request r;
-  int nt, mt;              // position tiles and row tiles of the request
+  int nt, mt;                // position tiles and row tiles of the request
   int head, tile_m, t0, t1;  // the item: key/value head, row tile, its position tiles
-  bool first_item, whole;  // the range's first item; it holds all of the row tile's positions
+  bool first_item, whole;    // the range's first item; it holds all of the row tile's positions
   bool started;
 
   __device__ void enter(const TreeAttnArgs& a) {
-    unsigned none = 0;
-    r = request_of(a, b, none);
     nt = Cut<TM, TN>::pos_tiles(r);
     mt = Cut<TM, TN>::row_tiles(a, r);
   }
-  __device__ Walk(const TreeAttnArgs& a, Spot s, int64_t begin, int64_t end)
-      : u(begin), u1(end), base(s.base), b(s.b), first_item(false), started(false) {
-    if (u < u1) enter(a);
+  __device__ Walk(const TreeAttnArgs& a, const Share& share, const Spot& s)
+      : u(0), u1(0), base(s.base), b(s.b), r(s.r), first_item(false), started(false) {
+    const int c = blockIdx.x;
+    if (c < share.ctas && s.b < a.bs) u = share.begin(c), u1 = share.begin(c + 1);
+    enter(a);
   }
   // The next item; false when the range is done.
   __device__ bool next(const TreeAttnArgs& a) {
     if (u >= u1) return false;
     while (r.n <= 0 || u - base >= static_cast<int64_t>(a.nkv) * mt * nt) {
       base += r.n > 0 ? static_cast<int64_t>(a.nkv) * mt * nt : 0;
-      ++b;
+      unsigned none = 0;
+      r = request_of(a, ++b, none);
       enter(a);
     }
     const int64_t local = u - base;
-    const int g = static_cast<int>(local / nt);
+    const int g = static_cast<int>(quotient(local, nt));
     t0 = static_cast<int>(local - static_cast<int64_t>(g) * nt);
     head = g / mt;
     tile_m = g - head * mt;
@@ -146,12 +177,36 @@ struct Walk {
   }
 };
 
+// What the joining kernel does for CTA c: the row tile that begins in c's range and ends in
+// a later one's (a CTA has at most one, its last item).
+struct JoinTask {
+  int b, head, tile_m, rows;  // rows 0: nothing
+  int first_slot, last_cta;   // parts: this slot, then slot 2 c' of CTAs c' = c + 1 .. last_cta
+};
+
+inline size_t join_tasks_bytes(int ctas) { return (sizeof(JoinTask) * ctas + 255) / 256 * 256; }
+
+// By one thread once the walk is done (its state is the last item's).
+template <int TM, int TN>
+__device__ __forceinline__ void write_join_task(const TreeAttnArgs& a, const Share& share, const Walk<TM, TN>& w) {
+  JoinTask task{0, 0, 0, 0, 0, 0};
+  if (w.started && w.t0 == 0 && w.t1 < w.nt) {
+    const int64_t end = w.u + (w.nt - w.t1);  // one past the row tile's last unit
+    int last = blockIdx.x + 1;
+    while (last + 1 < share.ctas && share.begin(last + 1) < end) ++last;
+    task = JoinTask{w.b, w.head, w.tile_m, min(TM, w.r.n * a.group - w.tile_m * TM),
+                    static_cast<int>(2 * blockIdx.x) + (w.first_item ? 0 : 1), last};
+  }
+  static_cast<JoinTask*>(a.tasks)[blockIdx.x] = task;
+}
+
 // The parent of node i >= 1: the previous node of a chain, else the node its id names.
 __device__ __forceinline__ int parent_of(const TreeAttnArgs& a, int b, int i, unsigned& err) {
   if (!a.tree_ids) return i - 1;
   const int64_t id = LDCG(a.tree_ids + static_cast<int64_t>(b) * (a.width - 1) + (i - 1));
-  const int64_t p = id >= 0 ? id / a.width : -1;
-  if (p < 0 || p >= i || id - p * a.width != i) {
+  const bool fits = id >= 0 && id < (1 << 30);
+  const uint32_t p = static_cast<uint32_t>(fits ? id : 0) / static_cast<uint32_t>(a.width);
+  if (!fits || p >= static_cast<uint32_t>(i) || static_cast<int>(id) - static_cast<int>(p) * a.width != i) {
     err |= FLASHMAP_DEVERR_TREE;
     return -1;  // no ancestors
   }
@@ -160,50 +215,58 @@ __device__ __forceinline__ int parent_of(const TreeAttnArgs& a, int b, int i, un
 
 // ------------------------------------------------------------------ joining split row tiles
 
-// Block c + 1 (x) looks at the border between CTAs c and c + 1 of the kernel before: if it
-// is the first border inside a row tile, the block joins that row tile's parts in CTA
-// order. Rows are spread over the blocks along y, a warp per row.
-constexpr int kJoinThreads = 256, kJoinY = 4;
+// Block (c, y) joins CTA c's task, a warp per row: the parts' maxima and sums first, a lane
+// per part, then the outputs weighted, four parts' loads in flight.
+constexpr int kJoinThreads = 256, kJoinY = 8;
 
-template <typename T, int HD, int TM, int TN>
+template <typename T, int HD, int TM>
 __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TreeAttnArgs a) {
-  __shared__ int64_t red[kJoinThreads / 32];
-  __shared__ Spot s_spot;
   pdl_trigger();
   pdl_wait();
-  const int G = gridDim.x + 1, c = blockIdx.x + 1;
-  unsigned none = 0;
-  Spot spot;
-  const int64_t units = locate<kJoinThreads, TM, TN>(a, c, G, spot, none, red, &s_spot);
-  const int64_t u = units * c / G;
-  if (u >= units) return;
-  const Request r = request_of(a, spot.b, none);
-  const int nt = Cut<TM, TN>::pos_tiles(r), mt = Cut<TM, TN>::row_tiles(a, r);
-  const int64_t g = (u - spot.base) / nt;
-  const int64_t g0 = spot.base + g * nt, g1 = g0 + nt;  // the row tile's units
-  if (u <= g0 || units * (c - 1) / G > g0) return;      // no border inside it, or not its first
-  const int head = static_cast<int>(g / mt), tile_m = static_cast<int>(g - static_cast<int64_t>(head) * mt);
-  const int rows = min(TM, r.n * a.group - tile_m * TM);
-  const int first = 2 * (c - 1) + (units * (c - 1) / G == g0 ? 0 : 1);  // CTA c - 1 may have begun elsewhere
+  const int c = blockIdx.x;
+  const int* raw = reinterpret_cast<const int*>(static_cast<const JoinTask*>(a.tasks) + c);
+  const JoinTask task{LDCG(raw), LDCG(raw + 1), LDCG(raw + 2), LDCG(raw + 3), LDCG(raw + 4), LDCG(raw + 5)};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int E = HD / 32;
-  for (int row = blockIdx.y * (kJoinThreads / 32) + warp; row < rows; row += kJoinY * (kJoinThreads / 32)) {
-    float m = -INFINITY, l = 0.f, o[E];
+  const int parts = task.last_cta - c + 1;
+  for (int row = blockIdx.y * (kJoinThreads / 32) + warp; row < task.rows; row += kJoinY * (kJoinThreads / 32)) {
+    auto at = [&](int p) {  // part p's row
+      return static_cast<int64_t>(p == 0 ? task.first_slot : 2 * (c + p)) * TM + row;
+    };
+    float m = -INFINITY;
+    float2 ml = make_float2(-INFINITY, 0.f);
+    for (int p = lane; p < parts; p += 32) {
+      ml = __ldcg(a.part_ml + at(p));
+      m = fmaxf(m, ml.x);
+    }
+    m = warp_max(m);
+    const float base = m == -INFINITY ? 0.f : m;
+    float l = 0.f, o[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = 0.f;
-    for (int p = c - 1; p < G && units * p / G < g1; ++p) {
-      if (units * p / G == units * (p + 1) / G) continue;
-      const int64_t at = static_cast<int64_t>(p == c - 1 ? first : 2 * p) * TM + row;
-      const float2 ml = __ldcg(a.part_ml + at);
-      const float mn = fmaxf(m, ml.x), base = mn == -INFINITY ? 0.f : mn;
-      const float f0 = exp2f(m - base), f1 = exp2f(ml.x - base);
-      l = l * f0 + ml.y * f1;
-      m = mn;
+    for (int p0 = 0; p0 < parts; p0 += 32) {
+      if (parts > 32) ml = p0 + lane < parts ? __ldcg(a.part_ml + at(p0 + lane)) : make_float2(-INFINITY, 0.f);
+      const float f = exp2f(ml.x - base);
+      l += ml.y * f;
+      const int n = min(32, parts - p0);
+      for (int p = 0; p < n; p += 4) {
+        float v[4][E];
 #pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = o[e] * f0 + LDCG(a.part_o + at * HD + lane + 32 * e) * f1;
+        for (int x = 0; x < 4; ++x)
+#pragma unroll
+          for (int e = 0; e < E; ++e)
+            v[x][e] = p + x < n ? LDCG(a.part_o + at(p0 + p + x) * HD + lane + 32 * e) : 0.f;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const float fx = __shfl_sync(0xffffffffu, f, (p + x) & 31);
+#pragma unroll
+          for (int e = 0; e < E; ++e) o[e] = fmaf(v[x][e], p + x < n ? fx : 0.f, o[e]);
+        }
+      }
     }
-    const int rr = tile_m * TM + row, i = rr / a.group, h = rr - i * a.group;
-    T* dst = static_cast<T*>(a.out) + ((static_cast<int64_t>(spot.b) * a.width + i) * a.nq + head * a.group + h) * HD;
+    l = warp_sum(l);
+    const int rr = task.tile_m * TM + row, i = rr / a.group, h = rr - i * a.group;
+    T* dst = static_cast<T*>(a.out) + ((static_cast<int64_t>(task.b) * a.width + i) * a.nq + task.head * a.group + h) * HD;
     const float inv = l > 0.f ? 1.f / l : 0.f;
 #pragma unroll
     for (int e = 0; e < E; ++e) dst[lane + 32 * e] = from_f32<T>(o[e] * inv);

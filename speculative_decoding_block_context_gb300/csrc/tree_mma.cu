@@ -43,6 +43,7 @@ struct MmaCfg {
 // TMEM columns: S (and then P) of lane m, buffer i at 128 m + 64 i; the lane's O at 256 + 128 m
 __device__ __forceinline__ constexpr uint32_t s_col(int m, int i) { return static_cast<uint32_t>(128 * m + 64 * i); }
 __device__ __forceinline__ constexpr uint32_t o_col(int m) { return static_cast<uint32_t>(256 + 128 * m); }
+constexpr int kLeastTiles = 4;  // position tiles a CTA takes at least
 constexpr int kRing = 64;  // position tiles whose readable blocks are remembered
 constexpr int kTmemCols = 512;
 
@@ -123,6 +124,24 @@ __device__ __noinline__ bool slow_wait(uint64_t* bar, uint32_t parity, volatile 
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
   return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) || slow_wait(bar, parity, abort);
 }
+// Two waits at the price of one when both are over.
+__device__ __forceinline__ bool warp_wait2(uint64_t* bar1, uint32_t parity1, uint64_t* bar2, uint32_t parity2,
+                                           volatile int* abort) {
+  const bool one = mbar_try_wait(bar1, parity1), two = mbar_try_wait(bar2, parity2);
+  if (__all_sync(0xffffffffu, one && two)) return true;
+  return slow_wait(bar1, parity1, abort) && slow_wait(bar2, parity2, abort);
+}
+// 32 bytes (aligned so): whole sectors even where a warp's lanes write rows of their own.
+__device__ __forceinline__ void store32(float* p, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -201,10 +220,8 @@ __global__ void __launch_bounds__(MmaCfg<HD, MT>::THREADS, 1)
 
   unsigned err = 0;
   Spot spot;
-  const int G = gridDim.x, c = blockIdx.x;
-  const int64_t units = locate<C::THREADS, TM, TN>(a, c, G, spot, err, red, &s_spot);
-  const int64_t u0 = units * c / G, u1 = units * (c + 1) / G;
-  Walk<TM, TN> w(a, spot, u0, u1);
+  const Share share = locate<C::THREADS, TM, TN>(a, kLeastTiles, spot, err, red, &s_spot);
+  Walk<TM, TN> w(a, share, spot);
   volatile int* ab = &abort_flag;
   // the item's rows, and whether each lane has rows of its own
   auto rows_of = [&]() { return min(TM, w.r.n * a.group - w.tile_m * TM); };
@@ -227,7 +244,7 @@ __global__ void __launch_bounds__(MmaCfg<HD, MT>::THREADS, 1)
     bool ok = true;
     while (ok && w.next(a)) {
       const int end = w.r.ctx + w.r.n;
-      const int64_t table = static_cast<int64_t>(LDCG(a.req_pool_idx + w.b)) * a.stride;
+      const int64_t table = static_cast<int64_t>(w.r.row) * a.stride;
       // Page ids are asked for 32 blocks of 16 positions (8 tiles) at a time, one batch ahead
       // of the tiles: a lookup takes longer than a tile's loads. Lane j holds block j.
       auto page_of = [&](int batch) {  // INT_MIN: nothing there
@@ -269,6 +286,7 @@ __global__ void __launch_bounds__(MmaCfg<HD, MT>::THREADS, 1)
       }
     }
     if (lane == 0) s_issued[warp] = seq;
+    if (threadIdx.x == 0) write_join_task(a, share, w);
   } else if (warp < 4) {
     // ---------------------------------------------------------------- products of lane m
     constexpr uint32_t idesc_s = idesc_bf16_f32(128, TN);
@@ -309,9 +327,9 @@ __global__ void __launch_bounds__(MmaCfg<HD, MT>::THREADS, 1)
         if (t < w.t1) {
           if (!own && t > w.t0 && !(ok = pass_k(t - 1))) break;
           const int q = seq + (t - w.t0), slot = q % KS, buf = ns & 1;
-          if (!(ok = warp_wait(&k_full[slot], (q / KS) & 1, ab))) break;
-          // the product that took P out of this buffer is done
-          if (ns >= 2 && !(ok = warp_wait(&pv_done[m][buf], ((ns >> 1) + 1) & 1, ab))) break;
+          // the tile, and the product that took P out of this buffer (the first two rounds'
+          // parity passes at once: nothing is in the buffers yet)
+          if (!(ok = warp_wait2(&k_full[slot], (q / KS) & 1, &pv_done[m][buf], ((ns >> 1) + 1) & 1, ab))) break;
           tc_fence_after();
           const uint32_t d = tmem + s_col(m, buf), klo = desc_lo(k0 + slot * C::TILE, 16);
 #pragma unroll
@@ -326,7 +344,7 @@ __global__ void __launch_bounds__(MmaCfg<HD, MT>::THREADS, 1)
         if (tv >= first) {
           if (!own && tv > w.t0 && !(ok = pass_v(tv - 1))) break;
           const int q = seq + (tv - w.t0), slot = q % VS, buf = np & 1;
-          if (!(ok = warp_wait(&v_full[slot], (q / VS) & 1, ab))) break;
+          if (!(ok = warp_wait2(&v_full[slot], (q / VS) & 1, &p_ready[m][buf], (np >> 1) & 1, ab))) break;
           const int left = end - tv * TN;  // positions of the tile that exist
           if (left < TN && left % box_rows) {
             // the last box's rows past the end hold whatever the page held: their weights are
@@ -338,7 +356,6 @@ __global__ void __launch_bounds__(MmaCfg<HD, MT>::THREADS, 1)
             fence_async_smem();
             __syncwarp();
           }
-          if (!(ok = warp_wait(&p_ready[m][buf], (np >> 1) & 1, ab))) break;
           // the item before has read its output
           if (tv == first && items > 0 && !(ok = warp_wait(&o_free[m], (items - 1) & 1, ab))) break;
           tc_fence_after();
@@ -449,7 +466,8 @@ __global__ void __launch_bounds__(MmaCfg<HD, MT>::THREADS, 1)
           }
           float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int x = 0; x < TN; ++x) tops[x & 3] = fmaxf(tops[x & 3], __uint_as_float(s[x]));
+          for (int x = 0; x < TN; x += 2)
+            tops[x / 2 & 3] = max3(tops[x / 2 & 3], __uint_as_float(s[x]), __uint_as_float(s[x + 1]));
           const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * k2;
           if (t == first) {
             mx = top;
@@ -525,7 +543,7 @@ __global__ void __launch_bounds__(MmaCfg<HD, MT>::THREADS, 1)
           f0 *= inv;
           f1 *= inv;
         }
-        const int64_t part = static_cast<int64_t>(2 * c + (w.first_item ? 0 : 1)) * TM + (own ? m * 128 : 0) + row;
+        const int64_t part = static_cast<int64_t>(2 * static_cast<int>(blockIdx.x) + (w.first_item ? 0 : 1)) * TM + (own ? m * 128 : 0) + row;
         __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + (q_row * a.nq + q_head) * HD;
 #pragma unroll
         for (int x = 0; x < HD; x += 32) {
@@ -556,8 +574,7 @@ __global__ void __launch_bounds__(MmaCfg<HD, MT>::THREADS, 1)
             }
           } else {
 #pragma unroll
-            for (int y = 0; y < 32; y += 4)
-              *reinterpret_cast<uint4*>(a.part_o + part * HD + x + y) = make_uint4(o[y], o[y + 1], o[y + 2], o[y + 3]);
+            for (int y = 0; y < 32; y += 8) store32(a.part_o + part * HD + x + y, o + y);
           }
         }
         if (live && !w.whole) a.part_ml[part] = make_float2(mx, l);
@@ -597,7 +614,7 @@ cudaError_t launch_mma(const Launch& L, const TreeAttnArgs& a, int G, const CUte
   if (e == cudaSuccess)
     e = launch_k(L, tree_mma_kernel<HD, MT>, dim3(G), dim3(C::THREADS), C::SMEM, kmap, vmap, a, box_rows);
   if (e == cudaSuccess && G > 1)
-    e = launch_k(L, tree_join_kernel<__nv_bfloat16, HD, C::TM, TN>, dim3(G - 1, kJoinY), dim3(kJoinThreads), 0, a);
+    e = launch_k(L, tree_join_kernel<__nv_bfloat16, HD, C::TM>, dim3(G - 1, kJoinY), dim3(kJoinThreads), 0, a);
   return e;
 }
 
@@ -608,12 +625,13 @@ int row_tiles_per_cta(int width, int group) { return width * group > 128 ? 2 : 1
 }  // namespace
 
 size_t tree_mma_bytes(int hd, int width, int group, int num_sms) {
-  return static_cast<size_t>(2 * num_sms) * 128 * row_tiles_per_cta(width, group) * (static_cast<size_t>(hd) * 4 + 8);
+  return join_tasks_bytes(num_sms) + static_cast<size_t>(2 * num_sms) * 128 * row_tiles_per_cta(width, group) * (static_cast<size_t>(hd) * 4 + 8);
 }
 
 cudaError_t tree_mma(const Launch& L, TreeAttnArgs a, void* workspace) {
   const int mt = row_tiles_per_cta(a.width, a.group), G = L.num_sms;
-  a.part_ml = static_cast<float2*>(workspace);
+  a.tasks = workspace;
+  a.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + join_tasks_bytes(G));
   a.part_o = reinterpret_cast<float*>(a.part_ml + static_cast<size_t>(2 * G) * 128 * mt);
   CUtensorMap kmap, vmap;
   std::string err;
