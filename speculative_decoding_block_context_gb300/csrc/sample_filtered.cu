@@ -10,9 +10,14 @@
 // integers: w 2^44 rounded, from an exponential good to about 1e-9, summed exactly in
 // 64 bits in whatever order.
 //
-// One CTA per row; the row is read from L2 in every pass. Borders are found by radix
-// selection on the logits' order-preserving bits, eight bits a pass, by count (top-k) or
-// by mass (top-p).
+// A row is held in the shared memory of a cluster of CTAs, so that it is read from memory
+// once. Its entries are sorted into bins by x = (m - l) * 11 log2(e) / T, eleven bins per
+// factor of two in weight; counts and masses of the bins say in which bins a border must
+// lie. Entries of lower x are kept whatever the border's exact place, so only their weights
+// are summed; the entries of the border's bins (at most kList) go to the first CTA, which
+// finds the exact border among them by radix selection and then the draw: among the listed
+// entries when nothing else is kept, else in one of the row's segments, whose warp walks it.
+// A border among more than kList equal logits takes a slower path over the row in memory.
 
 #include <algorithm>
 #include <climits>
@@ -24,8 +29,6 @@
 namespace fm {
 namespace {
 
-constexpr int kSfThreads = 1024;
-constexpr int kSfWarps = kSfThreads / 32;
 constexpr int kFixBits = 44;  // 393216 weights of at most 1 sum below 2^63
 
 __device__ __forceinline__ uint32_t order_key(float v) {
@@ -85,6 +88,7 @@ __device__ __forceinline__ V warp_incl(V v) {
   }
   return v;
 }
+template <int THREADS>
 __device__ __forceinline__ unsigned long long block_sum_u64(unsigned long long v, unsigned long long* red) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -92,7 +96,7 @@ __device__ __forceinline__ unsigned long long block_sum_u64(unsigned long long v
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
   unsigned long long t = 0;
-  for (int w = 0; w < kSfWarps; ++w) t += red[w];
+  for (int w = 0; w < THREADS / 32; ++w) t += red[w];
   return t;
 }
 
@@ -103,27 +107,26 @@ struct Border {
   int ties;
 };
 
-template <typename T>
-__global__ void __launch_bounds__(kSfThreads) sample_filtered_kernel(const SampleFilteredArgs a) {
-  __shared__ float2 tab[32];
-  __shared__ unsigned long long red[kSfWarps];
-  __shared__ unsigned long long hist[256];
+// The scratch of the slow path (the fast path's arrays serve).
+struct SlowScratch {
+  unsigned long long *red, *hist;  // [32], [256]
+  int* ties;                       // [32]
+};
+
+// A whole row by one CTA, read from memory in every pass: radix selection over all of it.
+template <typename T, int THREADS>
+__device__ __noinline__ void slow_row(const SampleFilteredArgs& a, int row, const float2* tab, SlowScratch scr) {
+  constexpr int kSfThreads = THREADS, kSfWarps = THREADS / 32;
   __shared__ uint32_t s_digit;
   __shared__ unsigned long long s_above;
   __shared__ int s_pick;
   __shared__ unsigned long long s_pickw;
-  pdl_trigger();
-  pdl_wait();
+  unsigned long long *red = scr.red, *hist = scr.hist;
+  int* s_ties = scr.ties;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  if (t < 32) {
-    const double h = exp2(t / 32.0);
-    tab[t].x = static_cast<float>(h);
-    tab[t].y = static_cast<float>(h - static_cast<double>(tab[t].x));
-  }
-  const int row = blockIdx.x, b = row / a.per, V = a.V;
+  const int b = row / a.per, V = a.V;
   const T* lr = static_cast<const T*>(a.logits) + static_cast<int64_t>(row) * a.ld;
   const float temp = a.temperature[b];
-  const bool greedy = !(temp > 0.f);
   int k = a.top_k ? a.top_k[b] : 0;
   if (k <= 0 || k > V) k = V;
   const float p = a.top_p ? a.top_p[b] : 1.f, mp = a.min_p ? a.min_p[b] : 0.f;
@@ -143,13 +146,6 @@ __global__ void __launch_bounds__(kSfThreads) sample_filtered_kernel(const Sampl
   __syncthreads();
   for (int w = 0; w < kSfWarps; ++w) best = max(best, red[w]);
   const int top = best ? static_cast<int>(0xffffffffu - static_cast<uint32_t>(best)) : 0;
-  if (greedy || best == 0) {
-    if (t == 0) {
-      a.tokens[row] = a.ids ? a.ids[top] : top;
-      if (a.probs) a.probs[row] = best ? 1.f : 0.f;
-    }
-    return;
-  }
   const uint32_t top_key = static_cast<uint32_t>(best >> 32);
   const float m = key_value(top_key);
   const Slope c = slope_of(temp);
@@ -161,7 +157,7 @@ __global__ void __launch_bounds__(kSfThreads) sample_filtered_kernel(const Sampl
     uint32_t prefix = 0;
     int left = k;
     for (int shift = 24; shift >= 0; shift -= 8) {
-      if (t < 256) hist[t] = 0;
+      for (int i = t; i < 256; i += THREADS) hist[i] = 0;
       __syncthreads();
       const uint32_t mask = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
       for (int j = t; j < V; j += kSfThreads) {
@@ -191,7 +187,7 @@ __global__ void __launch_bounds__(kSfThreads) sample_filtered_kernel(const Sampl
       const float l = load_logit(lr, j);
       if (usable(l) && order_key(l) > bd.key) s += weight_fix(l, m, c, tab);
     }
-    s = block_sum_u64(s, red);
+    s = block_sum_u64<THREADS>(s, red);
     if (bd.ties != INT_MAX && bd.key != 0) s += static_cast<unsigned long long>(bd.ties) * weight_fix(key_value(bd.key), m, c, tab);
     return s;
   };
@@ -201,7 +197,7 @@ __global__ void __launch_bounds__(kSfThreads) sample_filtered_kernel(const Sampl
     unsigned long long left = min(all, max(1ull, static_cast<unsigned long long>(want)));
     uint32_t prefix = 0;
     for (int shift = 24; shift >= 0; shift -= 8) {
-      if (t < 256) hist[t] = 0;
+      for (int i = t; i < 256; i += THREADS) hist[i] = 0;
       __syncthreads();
       const uint32_t mask = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
       for (int j = t; j < V; j += kSfThreads) {
@@ -239,7 +235,6 @@ __global__ void __launch_bounds__(kSfThreads) sample_filtered_kernel(const Sampl
   // the share that holds the draw is walked.
   const int share = ((V + kSfWarps - 1) / kSfWarps + 31) / 32 * 32;
   const int j0 = warp * share, j1 = min(V, j0 + share);
-  __shared__ int s_ties[kSfWarps];
   int ties_before = 0;
   if (border.ties != INT_MAX) {
     int n = 0;
@@ -310,11 +305,738 @@ __global__ void __launch_bounds__(kSfThreads) sample_filtered_kernel(const Sampl
   }
 }
 
+// ------------------------------------------------------------------ the cluster's row
+
+constexpr int kList = 1024;      // entries the first CTA can take
+constexpr int kBins = 512;       // bins of one window
+constexpr float kPerOctave = 11.f;  // 46 octaves (weights down to 2^-46) in 506 bins
+constexpr int kTopBins = 88;     // bins whose masses are exact (8 octaves); bins below: counted only
+constexpr int kLastBin = 507;    // from here on weights are 0
+constexpr int kMaxCluster = 8;
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t peer(const void* p, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ uint32_t peer_load(const uint32_t* p, uint32_t rank) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(peer(p, rank)) : "memory");
+  return v;
+}
+__device__ __forceinline__ unsigned long long peer_load(const unsigned long long* p, uint32_t rank) {
+  unsigned long long v;
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(peer(p, rank)) : "memory");
+  return v;
+}
+__device__ __forceinline__ void peer_store(uint32_t* p, uint32_t rank, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(peer(p, rank)), "r"(v) : "memory");
+}
+__device__ __forceinline__ void row_sync(int C) {  // every CTA of the row's cluster
+  if (C > 1) {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  } else {
+    __syncthreads();
+  }
+}
+
+// The first CTA's verdict, in every CTA's shared memory.
+struct Verdict {
+  uint32_t status;  // kDrawn, kWalk, kEarlier, kLater, kTopKDone
+  uint32_t key, tie_limit;  // kept: larger keys, and this key up to this index
+  uint32_t segment;         // where the draw lies
+  uint32_t rem_lo, rem_hi, total_lo, total_hi, above_lo, above_hi;
+};
+enum : uint32_t { kDrawn = 0, kWalk = 1, kEarlier = 2, kLater = 3, kTopKDone = 4 };
+
+template <int THREADS>
+struct RowSmem {
+  float2 tab[32];
+  uint32_t cnt[kBins];                 // this CTA's counts in the window's bins
+  unsigned long long mass[kTopBins];   // and masses of the top bins
+  uint32_t cc[kBins];                  // the row's counts up to and including a bin
+  float cm[kBins];                     // and masses (estimated from the counts below the top bins)
+  unsigned long long hist[256];
+  uint32_t lkey[kList], lidx[kList];
+  unsigned long long red[32], seg[THREADS / 32], all[kMaxCluster * (THREADS / 32)];
+  unsigned long long own[2];           // this CTA's sum; its kept-whatever-the-border sum
+  uint32_t found[kMaxCluster];         // listed entries per CTA
+  uint32_t top[kMaxCluster];           // largest logits per CTA (bits)
+  uint32_t n_list, digit, pick, pick_warp, s_bin;
+  unsigned long long left, pickw;
+  int ties[32];
+  Verdict v;
+};
+
+// The entries held in registers (E per thread; weight 0: none), sorted by key descending: the
+// key at which the running weight reaches `target` (1 at least, the sum at most); `target`
+// becomes what is still to take at that key.
+template <int E, int THREADS>
+__device__ __forceinline__ uint32_t reach(const uint32_t (&key)[E], const unsigned long long (&w)[E],
+                                          unsigned long long& target, RowSmem<THREADS>& S) {
+  const int t = threadIdx.x, lane = t & 31;
+  uint32_t prefix = 0;
+  for (int shift = 24; shift >= 0; shift -= 8) {
+    for (int i = t; i < 256; i += THREADS) S.hist[i] = 0;
+    __syncthreads();
+    const uint32_t mask = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      if (w[e] && (key[e] & mask) == prefix) atomicAdd(&S.hist[(key[e] >> shift) & 255], w[e]);
+    __syncthreads();
+    if (t < 32) {  // lane i holds digits 255 - 8 i down to 248 - 8 i
+      unsigned long long h[8], sum = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum += h[i] = S.hist[255 - 8 * lane - i];
+      const unsigned long long incl = warp_incl(sum);
+      const unsigned who = __ballot_sync(0xffffffffu, incl >= target);
+      if (lane == (who ? __ffs(who) - 1 : 31)) {
+        unsigned long long before = incl - sum;
+        int i = 0;
+        while (i < 7 && before + h[i] < target) before += h[i++];
+        S.digit = 255 - 8 * lane - i;
+        S.left = target - before;
+      }
+    }
+    __syncthreads();
+    prefix |= S.digit << shift;
+    target = S.left;
+  }
+  return prefix;
+}
+
+template <typename T, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kernel(const SampleFilteredArgs a, int C, int slice) {
+  constexpr int NW = THREADS / 32, E = kList / THREADS, VEC = 16 / sizeof(T);
+  extern __shared__ __align__(16) uint8_t row_raw[];
+  T* sl = reinterpret_cast<T*>(row_raw);
+  __shared__ RowSmem<THREADS> S;
+  pdl_trigger();
+  // a peer's shared memory may be written only once the peer runs
+  if (C > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  if (t < 32) {
+    const double h = exp2(t / 32.0);
+    S.tab[t].x = static_cast<float>(h);
+    S.tab[t].y = static_cast<float>(h - static_cast<double>(S.tab[t].x));
+  }
+  pdl_wait();
+  const int rank = C > 1 ? static_cast<int>(cluster_rank()) : 0;
+  const int row = blockIdx.x / C, b = row / a.per, V = a.V;
+  const T* lr = static_cast<const T*>(a.logits) + static_cast<int64_t>(row) * a.ld;
+  const float temp = __ldcg(a.temperature + b);
+  const bool greedy = !(temp > 0.f);
+  int k = a.top_k ? __ldcg(a.top_k + b) : 0;
+  if (k <= 0 || k > V) k = V;
+  const float p = a.top_p ? __ldcg(a.top_p + b) : 1.f, mp = a.min_p ? __ldcg(a.min_p + b) : 0.f;
+  float u = __ldcg(a.uniforms + row);
+  u = u > 0.f ? fminf(u, 0.99999994f) : 0.f;
+
+  // ---- the slice into shared memory, and its largest logit
+  const int j0 = rank * slice, n = max(0, min(slice, V - j0));
+  const T* src = lr + j0;
+  float mine = -INFINITY;
+  int done = 0;
+  if ((reinterpret_cast<uintptr_t>(lr) & 15) == 0) {
+    done = n / VEC * VEC;
+    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 4
+    for (int i = t * VEC; i < done; i += THREADS * VEC) {
+      const uint4 v = __ldcs(reinterpret_cast<const uint4*>(src + i));
+      *reinterpret_cast<uint4*>(sl + i) = v;
+      const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if constexpr (sizeof(T) == 4) {
+          mx[e] = fmaxf(mx[e], __uint_as_float(x[e]));
+        } else {
+          mx[e] = fmaxf(mx[e], fmaxf(__uint_as_float(x[e] << 16), __uint_as_float(x[e] & 0xffff0000u)));
+        }
+      }
+    }
+    mine = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+  }
+  for (int i = done + t; i < n; i += THREADS) {
+    const T v = src[i];
+    sl[i] = v;
+    mine = fmaxf(mine, to_f32<T>(v));
+  }
+  for (int i = n + t; i < slice; i += THREADS) sl[i] = from_f32<T>(-INFINITY);
+  mine = warp_max(mine);
+  if (lane == 0) S.red[warp] = __float_as_uint(mine);
+  for (int i = t; i < kBins; i += THREADS) S.cnt[i] = 0;
+  if (t < kTopBins) S.mass[t] = 0;
+  if (C > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  __syncthreads();
+  if (t < C) {
+    float x = -INFINITY;
+    for (int w = 0; w < NW; ++w) x = fmaxf(x, __uint_as_float(static_cast<uint32_t>(S.red[w])));
+    if (C > 1)
+      peer_store(&S.top[rank], t, __float_as_uint(x));
+    else
+      S.top[0] = __float_as_uint(x);
+  }
+  row_sync(C);
+  float m = -INFINITY;
+  for (int r = 0; r < C; ++r) m = fmaxf(m, __uint_as_float(S.top[r]));
+  m += 0.f;  // -0 counts as 0
+  auto emit = [&](int j, float prob) {
+    a.tokens[row] = a.ids ? a.ids[j] : j;
+    if (a.probs) a.probs[row] = prob;
+  };
+  if (!(m > -INFINITY)) {  // nothing to draw
+    if (rank == 0 && t == 0) emit(0, 0.f);
+    return;
+  }
+  auto at = [&](int i) { return to_f32<T>(sl[i]) + 0.f; };
+  if (greedy) {  // the first CTA that holds the largest logit finds its lowest index
+    int owner = 0;
+    while (__uint_as_float(S.top[owner]) != m) ++owner;
+    if (rank != owner) return;
+    int best = INT_MAX;
+    for (int i = t; i < n; i += THREADS)
+      if (at(i) == m) {
+        best = i;
+        break;
+      }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) best = min(best, __shfl_xor_sync(0xffffffffu, best, o));
+    if (lane == 0) S.ties[warp] = best;
+    __syncthreads();
+    if (t == 0) {
+      for (int w = 1; w < NW; ++w) best = min(best, S.ties[w]);
+      emit(j0 + best, 1.f);
+    }
+    return;
+  }
+  const Slope c = slope_of(temp);
+  const float per = c.hi * kPerOctave;
+  // place of a logit in units of bins, 0 at the largest; NaN and what has no weight at the end
+  auto place = [&](float l) { return l == m ? 0.f : fminf(__fmul_rn(__fsub_rn(m, l), per), 511.5f); };
+  const unsigned long long least =
+      mp > 0.f ? static_cast<unsigned long long>(ceil(static_cast<double>(fminf(mp, 1.f)) * (1ull << kFixBits))) : 0;
+
+  // ---- where the borders lie
+  const bool by_count = k < V, by_mass = p < 1.f;
+  unsigned long long whole = 0;  // the mass top-p takes its part of
+  float xa = INFINITY, xb = INFINITY;  // place < xa: kept whatever the border; xa <= place < xb: listed
+  uint32_t above_count = 0;            // entries of place < xa
+  bool count_left = by_count;          // top-k's border is still to be found
+  float x0 = 0.f, scale = 1.f;         // the window's bins: (place - x0) * scale
+  uint32_t base_count = 0;             // entries before the window
+  float base_mass = 0.f, shift_mass = 0.f;  // mass before the window; a correction once it is known exactly
+  int lim = kTopBins;                  // bins counted so far
+
+  // Counts the bins of the window from `b0` up to `b1`; in the first window, also the masses
+  // of its top bins and, when asked, the whole slice's mass.
+  auto count_bins = [&](int b0, int b1, bool want_mass) {
+    unsigned long long sum = 0;
+    float low = 0.f;
+    for (int i = t * VEC; i < slice; i += THREADS * VEC) {
+      const uint4 v = *reinterpret_cast<const uint4*>(sl + i);
+      const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const float l = (sizeof(T) == 4 ? __uint_as_float(x[e & 3])
+                                        : __uint_as_float(e & 1 ? x[e >> 1] & 0xffff0000u : x[e >> 1] << 16)) + 0.f;
+        const float pl = place(l), y = scale == 1.f ? pl : (pl - x0) * scale;
+        if (y >= b0 && y < b1) {
+          const int bin = static_cast<int>(y);
+          atomicAdd(&S.cnt[bin], 1u);
+          if (scale == 1.f && bin < kTopBins) {
+            const unsigned long long w = weight_fix(l, m, c, S.tab);
+            atomicAdd(&S.mass[bin], w);
+            sum += w;
+          }
+        } else if (want_mass) {
+          const float d = __fsub_rn(l, m);
+          float wf;
+          asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(wf) : "f"(__fmaf_rn(d, c.hi, d * c.lo)));
+          low += wf > 0.f ? wf : 0.f;  // NaN: nothing
+        }
+      }
+    }
+    if (want_mass) {
+      sum += __float2ull_rn(low * static_cast<float>(1ull << kFixBits));
+      sum = block_sum_u64<THREADS>(sum, S.red);
+      if (t == 0) S.own[0] = sum;
+    }
+  };
+  // The row's running counts and masses over the window's bins.
+  auto total_bins = [&]() {
+    constexpr int PER = kBins / THREADS;  // 2 or 1
+    uint32_t cs[PER], csum = 0;
+    float ms[PER], msum = 0.f;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int bin = t * PER + i;
+      cs[i] = 0;
+      ms[i] = 0.f;
+      if (bin < lim || scale != 1.f) {
+        for (int r = 0; r < C; ++r) cs[i] += C > 1 ? peer_load(&S.cnt[bin], r) : S.cnt[bin];
+        if (scale == 1.f && bin < kTopBins) {
+          unsigned long long q = 0;
+          for (int r = 0; r < C; ++r) q += C > 1 ? peer_load(&S.mass[bin], r) : S.mass[bin];
+          ms[i] = static_cast<float>(q) * (1.f / (1ull << kFixBits));
+        } else {
+          ms[i] = cs[i] * exp2f(-(x0 + (bin + 0.5f) / scale) / kPerOctave);
+        }
+      }
+      csum += cs[i];
+      msum += ms[i];
+    }
+    const uint32_t ci = warp_incl(csum);
+    const float mi = warp_incl(msum);
+    __syncthreads();
+    if (lane == 31) {
+      S.ties[warp] = ci;
+      S.red[warp] = __float_as_uint(mi);
+    }
+    __syncthreads();
+    uint32_t cb = base_count + ci - csum;
+    float mb = base_mass + shift_mass + mi - msum;
+    for (int w = 0; w < warp; ++w) {
+      cb += S.ties[w];
+      mb += __uint_as_float(static_cast<uint32_t>(S.red[w]));
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      cb += cs[i];
+      mb += ms[i];
+      S.cc[t * PER + i] = cb;
+      S.cm[t * PER + i] = mb;
+    }
+    __syncthreads();
+  };
+  // The first bin that reaches `k` entries (count) or the mass `goal`; kBins: none.
+  auto border_bin = [&](bool count, float goal) {
+    if (t == 0) S.s_bin = kBins;
+    __syncthreads();
+    for (int i = t; i < kBins; i += THREADS) {
+      const bool here = count ? S.cc[i] >= static_cast<uint32_t>(k) : S.cm[i] >= goal;
+      const bool before = i > 0 && (count ? S.cc[i - 1] >= static_cast<uint32_t>(k) : S.cm[i - 1] >= goal);
+      if (here && !before) atomicMin(&S.s_bin, static_cast<uint32_t>(i));
+    }
+    __syncthreads();
+    return static_cast<int>(S.s_bin);
+  };
+  auto goal_of = [&]() { return static_cast<float>(p * (static_cast<double>(whole) / (1ull << kFixBits))); };
+
+  // Back to the first window, all of its bins counted anew.
+  auto first_window = [&]() {
+    x0 = 0.f, scale = 1.f, base_count = 0, base_mass = 0.f, lim = kLastBin;
+    row_sync(C);  // the counts have been read
+    for (int i = t; i < kBins; i += THREADS) S.cnt[i] = 0;
+    if (t < kTopBins) S.mass[t] = 0;
+    __syncthreads();
+    count_bins(0, kLastBin, false);
+    row_sync(C);
+    total_bins();
+  };
+
+  bool slow = false;
+  int at_least = 0, at_most = kBins - 1;  // what earlier rounds have shown of the border's bin in this window
+  if (by_count || by_mass) {
+    if (V <= kList) {
+      xa = 0.f;
+      xb = kLastBin;
+      if (by_mass && !by_count) whole = ~0ull;  // summed from the list
+    } else {
+      count_bins(0, kTopBins, by_mass && !by_count);
+      row_sync(C);
+      if (by_mass && !by_count)
+        for (int r = 0; r < C; ++r) whole += C > 1 ? peer_load(&S.own[0], r) : S.own[0];
+      total_bins();
+    }
+  }
+  Verdict v{};
+  for (int round = 0;; ++round) {
+    // ---- choose the entries to list
+    if ((by_count || by_mass) && V > kList && !slow) {
+      for (;;) {
+        int B = border_bin(count_left, goal_of());
+        if (B == kBins && scale == 1.f && lim < kLastBin) {  // below the top bins: count the rest
+          row_sync(C);
+          count_bins(kTopBins, kLastBin, false);
+          lim = kLastBin;
+          row_sync(C);
+          total_bins();
+          continue;
+        }
+        if (B == kBins) B = scale == 1.f ? lim - 1 : kBins - 1;  // all that has weight, or a mass estimate too low
+        B = max(at_least, min(B, at_most));
+        if (S.cc[B] <= kList) {  // everything down to the border fits
+          int hi = B;
+          if (!count_left && hi + 1 < (scale == 1.f ? lim : kBins) && S.cc[hi + 1] <= kList) ++hi;
+          xa = 0.f;
+          xb = x0 + (hi + 1) / scale;
+          above_count = 0;
+          break;
+        }
+        const uint32_t before = B ? S.cc[B - 1] : base_count;
+        if (S.cc[B] - before <= kList) {
+          int lo = B, hi = B;
+          if (!count_left) {  // the masses are estimates: list the neighbours too where they fit
+            const int last = scale == 1.f ? lim - 1 : kBins - 1;
+            if (lo > 0 && S.cc[hi] - (lo > 1 ? S.cc[lo - 2] : base_count) <= kList) --lo;
+            if (hi < last && S.cc[hi + 1] - (lo > 0 ? S.cc[lo - 1] : base_count) <= kList) ++hi;
+          }
+          xa = x0 + lo / scale;
+          xb = x0 + (hi + 1) / scale;
+          above_count = lo > 0 ? S.cc[lo - 1] : base_count;
+          break;
+        }
+        if (scale != 1.f) {  // more than kList within 2^(1/5632): equal logits
+          slow = true;
+          break;
+        }
+        // a window on the bin alone
+        base_mass = B ? S.cm[B - 1] : base_mass + shift_mass;
+        shift_mass = 0.f;
+        base_count = before;
+        x0 += B / scale;
+        scale *= kBins;
+        at_least = 0, at_most = kBins - 1;
+        row_sync(C);  // the counts have been read
+        for (int i = t; i < kBins; i += THREADS) S.cnt[i] = 0;
+        __syncthreads();
+        count_bins(0, kBins, false);
+        row_sync(C);
+        total_bins();
+      }
+      if (slow) {
+        row_sync(C);  // peers have read this CTA's counts
+        if (rank == 0) slow_row<T, THREADS>(a, row, S.tab, SlowScratch{S.red, S.hist, S.ties});
+        return;
+      }
+    }
+
+    // ---- one pass: sum what is kept anyhow (per warp's segment), list the rest
+    if (t == 0) S.n_list = 0;
+    __syncthreads();
+    const int seg_len = slice / NW;
+    unsigned long long kept = 0, all = 0;
+    for (int i = warp * seg_len + lane * VEC; i < (warp + 1) * seg_len; i += 32 * VEC) {
+      const uint4 q = *reinterpret_cast<const uint4*>(sl + i);
+      const uint32_t x[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const float l = (sizeof(T) == 4 ? __uint_as_float(x[e & 3])
+                                        : __uint_as_float(e & 1 ? x[e >> 1] & 0xffff0000u : x[e >> 1] << 16)) + 0.f;
+        const float pl = place(l);
+        if (pl >= xb || pl >= kLastBin) continue;
+        if (pl < xa) {
+          const unsigned long long w = weight_fix(l, m, c, S.tab);
+          all += w;
+          if (w >= least) kept += w;
+        } else {
+          const uint32_t pos = atomicAdd(&S.n_list, 1u);
+          if (pos < kList) {
+            S.lkey[pos] = order_key(l);
+            S.lidx[pos] = j0 + i + e;
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      kept += __shfl_xor_sync(0xffffffffu, kept, o);
+      all += __shfl_xor_sync(0xffffffffu, all, o);
+    }
+    if (lane == 0) {
+      S.seg[warp] = kept;
+      S.red[warp] = all;
+    }
+    __syncthreads();
+    if (t == 0) {
+      unsigned long long s = 0;
+      for (int w = 0; w < NW; ++w) s += S.red[w];
+      S.own[1] = s;
+    }
+    if (t < C) {
+      if (C > 1)
+        peer_store(&S.found[rank], t, S.n_list);
+      else
+        S.found[0] = S.n_list;
+    }
+    row_sync(C);
+
+    // ---- the first CTA finds the border and the draw
+    const bool listed_only = xa == 0.f;
+    // a list from the top holds top-k's border for certain (a mass, estimated, may fall short
+    // of top-p's): the other CTAs are then no longer needed once it has been read
+    const bool early = listed_only && (V <= kList || count_left);
+    if (rank == 0) {
+      uint32_t key[E], idx[E];
+      unsigned long long w[E], one[E];
+      uint32_t start[kMaxCluster + 1];
+      start[0] = 0;
+      for (int r = 0; r < C; ++r) start[r + 1] = start[r] + S.found[r];
+      const uint32_t N = min(start[C], static_cast<uint32_t>(kList));
+      unsigned long long above = 0, zone = 0;
+      for (int r = 0; r < C; ++r) above += C > 1 ? peer_load(&S.own[1], r) : S.own[1];
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const uint32_t i = t + e * THREADS;
+        key[e] = idx[e] = 0;
+        w[e] = one[e] = 0;
+        if (i < N) {
+          int r = 0;
+          while (r + 1 < C && i >= start[r + 1]) ++r;
+          const uint32_t pos = i - start[r];
+          key[e] = C > 1 ? peer_load(&S.lkey[pos], r) : S.lkey[pos];
+          idx[e] = C > 1 ? peer_load(&S.lidx[pos], r) : S.lidx[pos];
+          w[e] = weight_fix(key_value(key[e]), m, c, S.tab);
+          one[e] = 1;
+          zone += w[e];
+        }
+      }
+      zone = block_sum_u64<THREADS>(zone, S.red);
+      if (early && C > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // lists read
+      v = Verdict{kDrawn, 0u, 0xffffffffu, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+      auto mass_if = [&](uint32_t K, unsigned long long ties) {  // of the keys above K, and ties at K
+        unsigned long long s = 0;
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          if (key[e] > K) s += w[e];
+        return block_sum_u64<THREADS>(s, S.red) + ties * weight_fix(key_value(K), m, c, S.tab);
+      };
+      unsigned long long ties = ~0ull, total = whole;  // ties: how many entries of v.key are kept
+      bool border = false;
+      if (by_mass && !by_count && V <= kList) total = zone;
+      if (count_left && static_cast<uint32_t>(k) - above_count < N) {
+        unsigned long long target = k - above_count;
+        v.key = reach<E, THREADS>(key, one, target, S);
+        ties = target;
+        border = true;
+        total = above + mass_if(v.key, ties);
+      } else if (count_left) {
+        total = above + zone;
+      }
+      if (by_mass) {
+        const double want = p > 0.f ? ceil(static_cast<double>(p) * static_cast<double>(total)) : 1.0;
+        const unsigned long long goal = min(total, max(1ull, static_cast<unsigned long long>(want)));
+        if (count_left && !listed_only) {
+          v.status = kTopKDone;  // top-p's border has still to be looked for, in another list
+          v.total_lo = static_cast<uint32_t>(total);
+          v.total_hi = static_cast<uint32_t>(total >> 32);
+        } else if (goal <= above) {
+          v.status = kEarlier;
+        } else if (goal - above > zone && xb < kLastBin) {
+          v.status = kLater;
+          above += zone;  // up to the list's end
+        } else {
+          unsigned long long target = min(goal - above, zone);
+          const uint32_t K = reach<E, THREADS>(key, w, target, S);
+          const unsigned long long wk = weight_fix(key_value(K), m, c, S.tab);
+          const unsigned long long take = wk ? (target + wk - 1) / wk : 1;
+          if (!border || K > v.key) {
+            v.key = K;
+            ties = take;
+          } else {
+            ties = min(ties, take);
+          }
+          border = true;
+        }
+        v.above_lo = static_cast<uint32_t>(above);
+        v.above_hi = static_cast<uint32_t>(above >> 32);
+      }
+      if (v.status == kDrawn) {
+        if (border) {
+          unsigned long long have = 0;
+          unsigned long long tie[E];
+          uint32_t inv[E];
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            tie[e] = one[e] && key[e] == v.key ? 1 : 0;
+            inv[e] = ~idx[e];
+            have += tie[e];
+          }
+          have = block_sum_u64<THREADS>(have, S.red);
+          if (ties < have) v.tie_limit = ~reach<E, THREADS>(inv, tie, ties, S);  // the ties-th lowest index
+        }
+        unsigned long long sum = 0;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const bool keep = w[e] >= least && (key[e] > v.key || (key[e] == v.key && idx[e] <= v.tie_limit));
+          if (!keep) w[e] = 0;
+          sum += w[e];
+        }
+        sum = block_sum_u64<THREADS>(sum, S.red);
+        if (listed_only) {
+          unsigned long long target =
+              static_cast<unsigned long long>(static_cast<double>(u) * static_cast<double>(sum)) + 1;
+          uint32_t inv[E];
+#pragma unroll
+          for (int e = 0; e < E; ++e) inv[e] = ~idx[e];
+          const uint32_t j = ~reach<E, THREADS>(inv, w, target, S);
+#pragma unroll
+          for (int e = 0; e < E; ++e)
+            if (w[e] && idx[e] == j) emit(j, static_cast<float>(static_cast<double>(w[e]) / static_cast<double>(sum)));
+        } else {
+          // the kept masses of the row's segments, and the one the draw falls in
+          v.status = kWalk;
+          for (int i = t; i < C * NW; i += THREADS) S.all[i] = C > 1 ? peer_load(&S.seg[i % NW], i / NW) : S.seg[i];
+          __syncthreads();
+#pragma unroll
+          for (int e = 0; e < E; ++e)
+            if (w[e]) atomicAdd(&S.all[idx[e] / static_cast<uint32_t>(seg_len)], w[e]);
+          __syncthreads();
+          if (t < 32) {
+            unsigned long long own4[kMaxCluster * NW / 32], s = 0;
+            constexpr int Q = kMaxCluster * NW / 32;
+#pragma unroll
+            for (int i = 0; i < Q; ++i) s += own4[i] = lane * Q + i < C * NW ? S.all[lane * Q + i] : 0;
+            const unsigned long long incl = warp_incl(s);
+            const unsigned long long tot = __shfl_sync(0xffffffffu, incl, 31);
+            const unsigned long long draw =
+                static_cast<unsigned long long>(static_cast<double>(u) * static_cast<double>(tot));
+            const unsigned who = __ballot_sync(0xffffffffu, incl > draw);
+            if (lane == (who ? __ffs(who) - 1 : 31)) {
+              unsigned long long before = incl - s;
+              int i = 0;
+              while (i < Q - 1 && before + own4[i] <= draw) before += own4[i++];
+              S.pick = lane * Q + i;
+              S.left = draw - before;
+              S.pickw = tot;
+            }
+          }
+          __syncthreads();
+          v.segment = S.pick;
+          v.rem_lo = static_cast<uint32_t>(S.left);
+          v.rem_hi = static_cast<uint32_t>(S.left >> 32);
+          v.total_lo = static_cast<uint32_t>(S.pickw);
+          v.total_hi = static_cast<uint32_t>(S.pickw >> 32);
+        }
+      }
+      if (early) {
+        if (C > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+        return;
+      }
+      __syncthreads();
+      constexpr int words = sizeof(Verdict) / 4;
+      const uint32_t* vw = reinterpret_cast<const uint32_t*>(&v);
+      if (t < C) {
+#pragma unroll
+        for (int i = 0; i < words; ++i) {
+          if (C > 1)
+            peer_store(reinterpret_cast<uint32_t*>(&S.v) + i, t, vw[i]);
+          else
+            reinterpret_cast<uint32_t*>(&S.v)[i] = vw[i];
+        }
+      }
+    } else if (early) {
+      // the first CTA goes on alone once it has read the lists
+      asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+      asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+      return;
+    }
+    row_sync(C);
+    v = S.v;
+    if (v.status == kDrawn) return;
+    if (v.status == kWalk) break;
+    // Another list: top-p's border now that top-k's mass is known, or a neighbouring bin, with
+    // the exact mass up to this list's start (or end) in place of its estimate.
+    if (round >= 64) {
+      if (rank == 0) slow_row<T, THREADS>(a, row, S.tab, SlowScratch{S.red, S.hist, S.ties});
+      return;
+    }
+    if (v.status == kTopKDone) {
+      whole = (static_cast<unsigned long long>(v.total_hi) << 32) | v.total_lo;
+      count_left = false;
+      if (scale != 1.f) first_window();
+      continue;
+    }
+    const unsigned long long known = (static_cast<unsigned long long>(v.above_hi) << 32) | v.above_lo;
+    const int lo = static_cast<int>((xa - x0) * scale), hi = static_cast<int>((xb - x0) * scale);
+    const int edge = v.status == kLater ? hi : lo;
+    const float delta = static_cast<float>(static_cast<double>(known) / (1ull << kFixBits)) -
+                        (edge > 0 ? S.cm[edge - 1] : base_mass + shift_mass);
+    shift_mass = scale == 1.f ? shift_mass + delta : delta;
+    if (v.status == kLater) at_least = hi; else at_most = lo - 1;
+    if (scale != 1.f && (at_least > kBins - 1 || at_most < 0)) {  // outside the window
+      at_least = 0, at_most = kBins - 1;
+      first_window();
+    } else {
+      __syncthreads();
+      for (int i = t; i < kBins; i += THREADS) S.cm[i] += delta;
+      if (scale != 1.f) base_mass += delta, shift_mass = 0.f;
+      __syncthreads();
+    }
+  }
+
+  // ---- the draw lies in one segment: its CTA's warps sum an eighth each, one walks its part
+  if (static_cast<int>(v.segment) / NW != rank) return;
+  const int seg_len = slice / NW, s0 = (v.segment % NW) * seg_len;
+  const int part = (seg_len / NW + 31) / 32 * 32;
+  const int i0 = s0 + min(seg_len, warp * part), i1 = s0 + min(seg_len, (warp + 1) * part);
+  auto kept_weight = [&](int i) -> unsigned long long {
+    const float l = i < i1 ? at(i) : -INFINITY;
+    const float pl = place(l);
+    if (pl >= xb || pl >= kLastBin) return 0;
+    if (pl >= xa) {
+      const uint32_t key = order_key(l);
+      if (!(key > v.key || (key == v.key && static_cast<uint32_t>(j0 + i) <= v.tie_limit))) return 0;
+    }
+    const unsigned long long w = weight_fix(l, m, c, S.tab);
+    return w >= least ? w : 0;
+  };
+  unsigned long long sum = 0;
+  for (int i = i0; i < i1; i += 32) sum += kept_weight(i + lane);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  __syncthreads();
+  if (lane == 0) S.red[warp] = sum;
+  __syncthreads();
+  unsigned long long before = 0;
+  for (int w = 0; w < warp; ++w) before += S.red[w];
+  const unsigned long long rem = (static_cast<unsigned long long>(v.rem_hi) << 32) | v.rem_lo;
+  if (!(before <= rem && rem < before + sum)) return;
+  for (int i = i0; i < i1; i += 32) {
+    const unsigned long long w = kept_weight(i + lane);
+    const unsigned long long incl = before + warp_incl(w);
+    const unsigned hit = __ballot_sync(0xffffffffu, incl > rem);
+    if (hit) {
+      if (lane == __ffs(hit) - 1) {
+        const unsigned long long total = (static_cast<unsigned long long>(v.total_hi) << 32) | v.total_lo;
+        emit(j0 + i + lane, static_cast<float>(static_cast<double>(w) / static_cast<double>(total)));
+      }
+      return;
+    }
+    before = __shfl_sync(0xffffffffu, incl, 31);
+  }
+}
+
+template <typename T>
+cudaError_t launch_sample(const Launch& L, const SampleFilteredArgs& a) {
+  // CTAs per row: slices of at most 40 KB where 8 CTAs allow it (four CTAs then share an SM),
+  // and more CTAs, down to 2048 entries each, while the rows alone do not fill the GPU.
+  int C = 1;
+  while (C < kMaxCluster && (static_cast<int64_t>(a.V) * sizeof(T) > 40960LL * C ||
+                             (static_cast<int64_t>(a.rows) * C < 2 * L.num_sms && a.V > 2048 * C)))
+    C *= 2;
+  const int unit = 32 * 8 * 16 / static_cast<int>(sizeof(T));  // a vector per lane and warp
+  const int slice = ((a.V + C - 1) / C + unit - 1) / unit * unit;
+  const size_t smem = static_cast<size_t>(slice) * sizeof(T);
+  // larger slices leave room for two CTAs per SM or one: wider CTAs then
+  const bool wide = smem > 49152;
+  auto kernel = wide ? sample_filtered_kernel<T, 512> : sample_filtered_kernel<T, 256>;
+  const int threads = wide ? 512 : 256;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  return launch_kc(L, kernel, dim3(static_cast<unsigned>(a.rows) * C), dim3(threads), smem, C, a, C, slice);
+}
+
 }  // namespace
 
 cudaError_t sample_filtered(const Launch& L, const SampleFilteredArgs& a) {
-  return launch_k(L, a.dtype == FLASHMAP_F32 ? sample_filtered_kernel<float> : sample_filtered_kernel<__nv_bfloat16>,
-                  dim3(a.rows), dim3(kSfThreads), 0, a);
+  return a.dtype == FLASHMAP_F32 ? launch_sample<float>(L, a) : launch_sample<__nv_bfloat16>(L, a);
 }
 
 }  // namespace fm
