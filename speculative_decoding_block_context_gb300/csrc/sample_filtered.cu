@@ -15,13 +15,14 @@
 // factor of two in weight; counts and masses of the bins say in which bins a border must
 // lie. Entries of lower x are kept whatever the border's exact place, so only their weights
 // are summed; the entries of the border's bins (at most kList) go to the first CTA, which
-// finds the exact border among them by radix selection and then the draw: among the listed
+// sorts them to find the exact border and then the draw: among the listed
 // entries when nothing else is kept, else in one of the row's segments, whose warp walks it.
 // A border among more than kList equal logits takes a slower path over the row in memory.
 
 #include <algorithm>
 #include <climits>
 #include <cstdint>
+#include <type_traits>
 
 #include "common.cuh"
 #include "internal.h"
@@ -362,53 +363,52 @@ struct RowSmem {
   unsigned long long mass[kTopBins];   // and masses of the top bins
   uint32_t cc[kBins];                  // the row's counts up to and including a bin
   float cm[kBins];                     // and masses (estimated from the counts below the top bins)
-  unsigned long long hist[256];
-  uint32_t lkey[kList], lidx[kList];
+  unsigned long long ent[kList];       // listed entries: order_key << 32 | ~index
   unsigned long long red[32], seg[THREADS / 32], all[kMaxCluster * (THREADS / 32)];
   unsigned long long own[2];           // this CTA's sum; its kept-whatever-the-border sum
   uint32_t found[kMaxCluster];         // listed entries per CTA
   uint32_t top[kMaxCluster];           // largest logits per CTA (bits)
-  uint32_t n_list, digit, pick, pick_warp, s_bin;
+  uint32_t n_list, pick, s_bin;
   unsigned long long left, pickw;
   int ties[32];
   Verdict v;
 };
 
-// The entries held in registers (E per thread; weight 0: none), sorted by key descending: the
-// key at which the running weight reaches `target` (1 at least, the sum at most); `target`
-// becomes what is still to take at that key.
-template <int E, int THREADS>
-__device__ __forceinline__ uint32_t reach(const uint32_t (&key)[E], const unsigned long long (&w)[E],
-                                          unsigned long long& target, RowSmem<THREADS>& S) {
-  const int t = threadIdx.x, lane = t & 31;
-  uint32_t prefix = 0;
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int i = t; i < 256; i += THREADS) S.hist[i] = 0;
-    __syncthreads();
-    const uint32_t mask = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-      if (w[e] && (key[e] & mask) == prefix) atomicAdd(&S.hist[(key[e] >> shift) & 255], w[e]);
-    __syncthreads();
-    if (t < 32) {  // lane i holds digits 255 - 8 i down to 248 - 8 i
-      unsigned long long h[8], sum = 0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) sum += h[i] = S.hist[255 - 8 * lane - i];
-      const unsigned long long incl = warp_incl(sum);
-      const unsigned who = __ballot_sync(0xffffffffu, incl >= target);
-      if (lane == (who ? __ffs(who) - 1 : 31)) {
-        unsigned long long before = incl - sum;
-        int i = 0;
-        while (i < 7 && before + h[i] < target) before += h[i++];
-        S.digit = 255 - 8 * lane - i;
-        S.left = target - before;
+// Sorts ent[0 .. n) descending, n a power of two (64 at least), by a bitonic network; exchanges
+// at distances up to 32 stay within a warp's 64 entries.
+template <int THREADS>
+__device__ __forceinline__ void sort_entries(unsigned long long* ent, int n) {
+  const int t = threadIdx.x;
+  __syncthreads();
+  for (int k = 2; k <= n; k <<= 1) {
+    for (int j = k >> 1; j > 0; j >>= 1) {
+      for (int p = t; p < n / 2; p += THREADS) {
+        const int i = 2 * p - (p & (j - 1)), o = i + j;
+        const unsigned long long x = ent[i], y = ent[o];
+        if ((x < y) == ((i & k) == 0)) {
+          ent[i] = y;
+          ent[o] = x;
+        }
       }
+      if (j > 32 || (j == 1 && k >= 64)) __syncthreads(); else __syncwarp();
     }
-    __syncthreads();
-    prefix |= S.digit << shift;
-    target = S.left;
   }
-  return prefix;
+  __syncthreads();
+}
+
+// Inclusive sums over the block of E consecutive values per thread, in place.
+template <int E, int THREADS>
+__device__ __forceinline__ void scan_values(unsigned long long (&v)[E], unsigned long long* red) {
+#pragma unroll
+  for (int e = 1; e < E; ++e) v[e] += v[e - 1];
+  const unsigned long long incl = warp_incl(v[E - 1]);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 31) red[threadIdx.x >> 5] = incl;
+  __syncthreads();
+  unsigned long long before = incl - v[E - 1];
+  for (int w = 0; w < static_cast<int>(threadIdx.x >> 5); ++w) before += red[w];
+#pragma unroll
+  for (int e = 0; e < E; ++e) v[e] += before;
 }
 
 template <typename T, int THREADS>
@@ -486,6 +486,18 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
   float m = -INFINITY;
   for (int r = 0; r < C; ++r) m = fmaxf(m, __uint_as_float(S.top[r]));
   m += 0.f;  // -0 counts as 0
+  auto row_total = [&](const auto* x) {  // of the same variable of every CTA, all loads in flight
+    auto s = *x;
+    if (C > 1) {
+      std::remove_reference_t<decltype(s)> y[kMaxCluster];
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r) y[r] = r < C ? peer_load(x, r) : 0;
+      s = 0;
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r) s += y[r];
+    }
+    return s;
+  };
   auto emit = [&](int j, float prob) {
     a.tokens[row] = a.ids ? a.ids[j] : j;
     if (a.probs) a.probs[row] = prob;
@@ -579,10 +591,9 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
       cs[i] = 0;
       ms[i] = 0.f;
       if (bin < lim || scale != 1.f) {
-        for (int r = 0; r < C; ++r) cs[i] += C > 1 ? peer_load(&S.cnt[bin], r) : S.cnt[bin];
+        cs[i] = row_total(&S.cnt[bin]);
         if (scale == 1.f && bin < kTopBins) {
-          unsigned long long q = 0;
-          for (int r = 0; r < C; ++r) q += C > 1 ? peer_load(&S.mass[bin], r) : S.mass[bin];
+          const unsigned long long q = row_total(&S.mass[bin]);
           ms[i] = static_cast<float>(q) * (1.f / (1ull << kFixBits));
         } else {
           ms[i] = cs[i] * exp2f(-(x0 + (bin + 0.5f) / scale) / kPerOctave);
@@ -641,7 +652,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
   };
 
   bool slow = false;
-  int at_least = 0, at_most = kBins - 1;  // what earlier rounds have shown of the border's bin in this window
+  // What earlier rounds have shown of the border's bin, in the first window and in a later one.
+  int first_least = 0, first_most = kBins - 1, at_least = 0, at_most = kBins - 1;
   if (by_count || by_mass) {
     if (V <= kList) {
       xa = 0.f;
@@ -651,7 +663,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
       count_bins(0, kTopBins, by_mass && !by_count);
       row_sync(C);
       if (by_mass && !by_count)
-        for (int r = 0; r < C; ++r) whole += C > 1 ? peer_load(&S.own[0], r) : S.own[0];
+        whole = row_total(&S.own[0]);
       total_bins();
     }
   }
@@ -670,7 +682,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
           continue;
         }
         if (B == kBins) B = scale == 1.f ? lim - 1 : kBins - 1;  // all that has weight, or a mass estimate too low
-        B = max(at_least, min(B, at_most));
+        B = scale == 1.f ? max(first_least, min(B, first_most)) : max(at_least, min(B, at_most));
         if (S.cc[B] <= kList) {  // everything down to the border fits
           int hi = B;
           if (!count_left && hi + 1 < (scale == 1.f ? lim : kBins) && S.cc[hi + 1] <= kList) ++hi;
@@ -712,7 +724,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
       }
       if (slow) {
         row_sync(C);  // peers have read this CTA's counts
-        if (rank == 0) slow_row<T, THREADS>(a, row, S.tab, SlowScratch{S.red, S.hist, S.ties});
+        if (rank == 0) slow_row<T, THREADS>(a, row, S.tab, SlowScratch{S.red, S.ent, S.ties});
         return;
       }
     }
@@ -737,10 +749,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
           if (w >= least) kept += w;
         } else {
           const uint32_t pos = atomicAdd(&S.n_list, 1u);
-          if (pos < kList) {
-            S.lkey[pos] = order_key(l);
-            S.lidx[pos] = j0 + i + e;
-          }
+          if (pos < kList)
+            S.ent[pos] = (static_cast<unsigned long long>(order_key(l)) << 32) | ~static_cast<uint32_t>(j0 + i + e);
         }
       }
     }
@@ -773,51 +783,75 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
     // of top-p's): the other CTAs are then no longer needed once it has been read
     const bool early = listed_only && (V <= kList || count_left);
     if (rank == 0) {
-      uint32_t key[E], idx[E];
-      unsigned long long w[E], one[E];
       uint32_t start[kMaxCluster + 1];
       start[0] = 0;
-      for (int r = 0; r < C; ++r) start[r + 1] = start[r] + S.found[r];
-      const uint32_t N = min(start[C], static_cast<uint32_t>(kList));
-      unsigned long long above = 0, zone = 0;
-      for (int r = 0; r < C; ++r) above += C > 1 ? peer_load(&S.own[1], r) : S.own[1];
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const uint32_t i = t + e * THREADS;
-        key[e] = idx[e] = 0;
-        w[e] = one[e] = 0;
-        if (i < N) {
-          int r = 0;
+      for (int r = 0; r < kMaxCluster; ++r) start[r + 1] = start[r] + (r < C ? S.found[r] : 0);
+      const int N = static_cast<int>(min(start[kMaxCluster], static_cast<uint32_t>(kList)));
+      int n2 = 64;
+      while (n2 < N) n2 *= 2;
+      unsigned long long above = row_total(&S.own[1]);
+      {
+        unsigned long long got[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const uint32_t i = t + e * THREADS;
+          got[e] = 0;
+          if (i < start[1] || i >= static_cast<uint32_t>(N)) continue;  // this CTA's own lie in place
+          int r = 1;
           while (r + 1 < C && i >= start[r + 1]) ++r;
-          const uint32_t pos = i - start[r];
-          key[e] = C > 1 ? peer_load(&S.lkey[pos], r) : S.lkey[pos];
-          idx[e] = C > 1 ? peer_load(&S.lidx[pos], r) : S.lidx[pos];
-          w[e] = weight_fix(key_value(key[e]), m, c, S.tab);
-          one[e] = 1;
-          zone += w[e];
+          got[e] = peer_load(&S.ent[i - start[r]], r);
+        }
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const int i = t + e * THREADS;
+          if (i >= static_cast<int>(start[1]) && i < n2) S.ent[i] = got[e];
         }
       }
-      zone = block_sum_u64<THREADS>(zone, S.red);
       if (early && C > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // lists read
-      v = Verdict{kDrawn, 0u, 0xffffffffu, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-      auto mass_if = [&](uint32_t K, unsigned long long ties) {  // of the keys above K, and ties at K
-        unsigned long long s = 0;
+      sort_entries<THREADS>(S.ent, n2);
+      // entry t E + e: its weight, and the weights up to and including it
+      unsigned long long w[E], incl[E];
 #pragma unroll
-        for (int e = 0; e < E; ++e)
-          if (key[e] > K) s += w[e];
-        return block_sum_u64<THREADS>(s, S.red) + ties * weight_fix(key_value(K), m, c, S.tab);
+      for (int e = 0; e < E; ++e) {
+        const int i = t * E + e;
+        w[e] = incl[e] = i < N ? weight_fix(key_value(static_cast<uint32_t>(S.ent[i] >> 32)), m, c, S.tab) : 0;
+      }
+      scan_values<E, THREADS>(incl, S.red);
+      // the sum over the first x entries (x >= 1)
+      auto upto = [&](int x) {
+        if ((x - 1) / E == t) {
+#pragma unroll
+          for (int e = 0; e < E; ++e)
+            if ((x - 1) % E == e) S.left = incl[e];
+        }
+        __syncthreads();
+        const unsigned long long s = S.left;
+        __syncthreads();
+        return s;
       };
-      unsigned long long ties = ~0ull, total = whole;  // ties: how many entries of v.key are kept
-      bool border = false;
-      if (by_mass && !by_count && V <= kList) total = zone;
-      if (count_left && static_cast<uint32_t>(k) - above_count < N) {
-        unsigned long long target = k - above_count;
-        v.key = reach<E, THREADS>(key, one, target, S);
-        ties = target;
-        border = true;
-        total = above + mass_if(v.key, ties);
-      } else if (count_left) {
-        total = above + zone;
+      // how many leading entries satisfy a condition that once false stays false
+      auto leading = [&](auto cond) {
+        int x = 0;
+#pragma unroll
+        for (int e = 0; e < E; ++e) x += t * E + e < N && cond(w[e], incl[e]) ? 1 : 0;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+        if (lane == 0) S.ties[warp] = x;
+        __syncthreads();
+        x = 0;
+        for (int q = 0; q < NW; ++q) x += S.ties[q];
+        __syncthreads();
+        return x;
+      };
+      v = Verdict{kDrawn, 0u, 0xffffffffu, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+      const unsigned long long zone = N ? upto(N) : 0;
+      unsigned long long total = by_mass && !by_count && V <= kList ? zone : whole;
+      int keep = N;  // the first so many entries are kept
+      if (count_left) {
+        const uint32_t want = k - above_count;
+        if (want < static_cast<uint32_t>(N)) keep = want;
+        total = above + (keep ? upto(keep) : 0);
       }
       if (by_mass) {
         const double want = p > 0.f ? ceil(static_cast<double>(p) * static_cast<double>(total)) : 1.0;
@@ -832,74 +866,78 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
           v.status = kLater;
           above += zone;  // up to the list's end
         } else {
-          unsigned long long target = min(goal - above, zone);
-          const uint32_t K = reach<E, THREADS>(key, w, target, S);
-          const unsigned long long wk = weight_fix(key_value(K), m, c, S.tab);
-          const unsigned long long take = wk ? (target + wk - 1) / wk : 1;
-          if (!border || K > v.key) {
-            v.key = K;
-            ties = take;
-          } else {
-            ties = min(ties, take);
-          }
-          border = true;
+          const unsigned long long rest = goal - above;
+          keep = min(keep, leading([&](unsigned long long wi, unsigned long long in) { return in - wi < rest; }));
         }
         v.above_lo = static_cast<uint32_t>(above);
         v.above_hi = static_cast<uint32_t>(above >> 32);
       }
       if (v.status == kDrawn) {
-        if (border) {
-          unsigned long long have = 0;
-          unsigned long long tie[E];
-          uint32_t inv[E];
+        // min-p is asked of each entry, here as in the walk below
+        if (keep > 0) {
+          v.key = static_cast<uint32_t>(S.ent[keep - 1] >> 32);
+          v.tie_limit = ~static_cast<uint32_t>(S.ent[keep - 1]);
+        } else {
+          v.key = 0xffffffffu;  // none of the list
+          v.tie_limit = 0;
+        }
+        if (listed_only) {
+          // the kept entries in index order: the draw is the first whose sum passes it
+          unsigned long long sum = 0;
+#pragma unroll
+          for (int e = 0; e < E; ++e) sum += t * E + e < keep && w[e] >= least ? w[e] : 0;
+          sum = block_sum_u64<THREADS>(sum, S.red);
+          const unsigned long long draw =
+              static_cast<unsigned long long>(static_cast<double>(u) * static_cast<double>(sum));
+          int k2 = 64;
+          while (k2 < keep) k2 *= 2;
+          unsigned long long x[E];
 #pragma unroll
           for (int e = 0; e < E; ++e) {
-            tie[e] = one[e] && key[e] == v.key ? 1 : 0;
-            inv[e] = ~idx[e];
-            have += tie[e];
+            const int i = t * E + e;
+            x[e] = i < keep ? (S.ent[i] << 32) | (S.ent[i] >> 32) : 0;
           }
-          have = block_sum_u64<THREADS>(have, S.red);
-          if (ties < have) v.tie_limit = ~reach<E, THREADS>(inv, tie, ties, S);  // the ties-th lowest index
-        }
-        unsigned long long sum = 0;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const bool keep = w[e] >= least && (key[e] > v.key || (key[e] == v.key && idx[e] <= v.tie_limit));
-          if (!keep) w[e] = 0;
-          sum += w[e];
-        }
-        sum = block_sum_u64<THREADS>(sum, S.red);
-        if (listed_only) {
-          unsigned long long target =
-              static_cast<unsigned long long>(static_cast<double>(u) * static_cast<double>(sum)) + 1;
-          uint32_t inv[E];
-#pragma unroll
-          for (int e = 0; e < E; ++e) inv[e] = ~idx[e];
-          const uint32_t j = ~reach<E, THREADS>(inv, w, target, S);
+          __syncthreads();
 #pragma unroll
           for (int e = 0; e < E; ++e)
-            if (w[e] && idx[e] == j) emit(j, static_cast<float>(static_cast<double>(w[e]) / static_cast<double>(sum)));
+            if (t * E + e < k2) S.ent[t * E + e] = x[e];
+          sort_entries<THREADS>(S.ent, k2);
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            const int i = t * E + e;
+            w[e] = i < keep ? weight_fix(key_value(static_cast<uint32_t>(S.ent[i])), m, c, S.tab) : 0;
+            if (w[e] < least) w[e] = 0;
+            incl[e] = w[e];
+          }
+          scan_values<E, THREADS>(incl, S.red);
+#pragma unroll
+          for (int e = 0; e < E; ++e)
+            if (incl[e] > draw && incl[e] - w[e] <= draw)
+              emit(~static_cast<uint32_t>(S.ent[t * E + e] >> 32),
+                   static_cast<float>(static_cast<double>(w[e]) / static_cast<double>(sum)));
         } else {
           // the kept masses of the row's segments, and the one the draw falls in
           v.status = kWalk;
           for (int i = t; i < C * NW; i += THREADS) S.all[i] = C > 1 ? peer_load(&S.seg[i % NW], i / NW) : S.seg[i];
           __syncthreads();
 #pragma unroll
-          for (int e = 0; e < E; ++e)
-            if (w[e]) atomicAdd(&S.all[idx[e] / static_cast<uint32_t>(seg_len)], w[e]);
+          for (int e = 0; e < E; ++e) {
+            const int i = t * E + e;
+            if (i < keep && w[e] >= least) atomicAdd(&S.all[~static_cast<uint32_t>(S.ent[i]) / static_cast<uint32_t>(seg_len)], w[e]);
+          }
           __syncthreads();
           if (t < 32) {
-            unsigned long long own4[kMaxCluster * NW / 32], s = 0;
             constexpr int Q = kMaxCluster * NW / 32;
+            unsigned long long own4[Q], s = 0;
 #pragma unroll
             for (int i = 0; i < Q; ++i) s += own4[i] = lane * Q + i < C * NW ? S.all[lane * Q + i] : 0;
-            const unsigned long long incl = warp_incl(s);
-            const unsigned long long tot = __shfl_sync(0xffffffffu, incl, 31);
+            const unsigned long long in = warp_incl(s);
+            const unsigned long long tot = __shfl_sync(0xffffffffu, in, 31);
             const unsigned long long draw =
                 static_cast<unsigned long long>(static_cast<double>(u) * static_cast<double>(tot));
-            const unsigned who = __ballot_sync(0xffffffffu, incl > draw);
+            const unsigned who = __ballot_sync(0xffffffffu, in > draw);
             if (lane == (who ? __ffs(who) - 1 : 31)) {
-              unsigned long long before = incl - s;
+              unsigned long long before = in - s;
               int i = 0;
               while (i < Q - 1 && before + own4[i] <= draw) before += own4[i++];
               S.pick = lane * Q + i;
@@ -944,7 +982,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
     // Another list: top-p's border now that top-k's mass is known, or a neighbouring bin, with
     // the exact mass up to this list's start (or end) in place of its estimate.
     if (round >= 64) {
-      if (rank == 0) slow_row<T, THREADS>(a, row, S.tab, SlowScratch{S.red, S.hist, S.ties});
+      if (rank == 0) slow_row<T, THREADS>(a, row, S.tab, SlowScratch{S.red, S.ent, S.ties});
       return;
     }
     if (v.status == kTopKDone) {
@@ -959,11 +997,17 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
     const float delta = static_cast<float>(static_cast<double>(known) / (1ull << kFixBits)) -
                         (edge > 0 ? S.cm[edge - 1] : base_mass + shift_mass);
     shift_mass = scale == 1.f ? shift_mass + delta : delta;
-    if (v.status == kLater) at_least = hi; else at_most = lo - 1;
-    if (scale != 1.f && (at_least > kBins - 1 || at_most < 0)) {  // outside the window
-      at_least = 0, at_most = kBins - 1;
+    if (scale != 1.f && (v.status == kLater ? hi > kBins - 1 : lo < 1)) {  // outside the window
+      if (v.status == kLater)
+        first_least = static_cast<int>(x0) + 1;
+      else
+        first_most = static_cast<int>(x0) - 1;
       first_window();
     } else {
+      if (v.status == kLater)
+        (scale == 1.f ? first_least : at_least) = hi;
+      else
+        (scale == 1.f ? first_most : at_most) = lo - 1;
       __syncthreads();
       for (int i = t; i < kBins; i += THREADS) S.cm[i] += delta;
       if (scale != 1.f) base_mass += delta, shift_mass = 0.f;
