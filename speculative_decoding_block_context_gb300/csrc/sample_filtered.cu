@@ -40,37 +40,68 @@ __device__ __forceinline__ float key_value(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
 }
 
-// log2(e) / T in two float32 parts.
+// 2^(i / 32) in two float32 parts.
+__constant__ const float2 kPowers[32] = {
+    {0x1.0000000000000p+0f, 0x0.0p+0f}, {0x1.059b0e0000000p+0f, -0x1.9d4f520000000p-25f},
+    {0x1.0b55860000000p+0f, 0x1.9f31220000000p-25f}, {0x1.11301e0000000p+0f, -0x1.fdb4960000000p-25f},
+    {0x1.172b840000000p+0f, -0x1.c157420000000p-27f}, {0x1.1d48740000000p+0f, -0x1.d2e8ca0000000p-25f},
+    {0x1.2387a60000000p+0f, 0x1.ceac480000000p-25f}, {0x1.29e9e00000000p+0f, -0x1.5c04240000000p-25f},
+    {0x1.306fe00000000p+0f, 0x1.4636e20000000p-25f}, {0x1.371a740000000p+0f, -0x1.18aac60000000p-25f},
+    {0x1.3dea640000000p+0f, 0x1.8246840000000p-25f}, {0x1.44e0860000000p+0f, 0x1.8624b40000000p-30f},
+    {0x1.4bfdae0000000p+0f, -0x1.593abc0000000p-25f}, {0x1.5342b60000000p+0f, -0x1.2c56100000000p-25f},
+    {0x1.5ab07e0000000p+0f, -0x1.5bd5ec0000000p-27f}, {0x1.6247ec0000000p+0f, -0x1.f8b5500000000p-25f},
+    {0x1.6a09e60000000p+0f, 0x1.9fcef40000000p-26f}, {0x1.71f75e0000000p+0f, 0x1.1d8bee0000000p-25f},
+    {0x1.7a11480000000p+0f, -0x1.829fd00000000p-25f}, {0x1.82589a0000000p+0f, -0x1.accc7c0000000p-26f},
+    {0x1.8ace540000000p+0f, 0x1.15506e0000000p-27f}, {0x1.93737c0000000p+0f, -0x1.e647440000000p-25f},
+    {0x1.9c49180000000p+0f, 0x1.51f8480000000p-27f}, {0x1.a5503c0000000p+0f, -0x1.b83b540000000p-25f},
+    {0x1.ae89fa0000000p+0f, -0x1.a94b140000000p-26f}, {0x1.b7f7700000000p+0f, -0x1.a094380000000p-25f},
+    {0x1.c199be0000000p+0f, -0x1.3d56b20000000p-27f}, {0x1.cb720e0000000p+0f, -0x1.8837cc0000000p-27f},
+    {0x1.d5818e0000000p+0f, -0x1.822dbc0000000p-27f}, {0x1.dfc9740000000p+0f, -0x1.908c940000000p-25f},
+    {0x1.ea4afa0000000p+0f, 0x1.52486c0000000p-27f}, {0x1.f507660000000p+0f, -0x1.246eb00000000p-26f}};
+
+// log2(e) / T in two float32 parts: the quotient of log2(e)'s first part, then that of what
+// it leaves and the second part.
 struct Slope {
   float hi, lo;
 };
 __device__ __forceinline__ Slope slope_of(float T) {
-  const double c = 1.4426950408889634074 / static_cast<double>(T);
+  constexpr float e_hi = 0x1.715476p+0f, e_lo = 0x1.4ae0c0p-26f;
   Slope s;
-  s.hi = static_cast<float>(c);
-  s.lo = isinf(s.hi) ? 0.f : static_cast<float>(c - static_cast<double>(s.hi));
+  s.hi = __fdiv_rn(e_hi, T);
+  s.lo = __fdiv_rn(__fmaf_rn(-s.hi, T, e_hi) + e_lo, T);
+  if (!(fabsf(s.lo) < 1e30f)) s.lo = 0.f;  // T so small or large that the quotient overflows
   return s;
 }
 
 // exp((l - m) / T) 2^44, rounded. With x = (l - m) log2(e) / T carried in two parts,
 // x = n / 32 + r, |r| <= 1/64: 2^x = 2^(n / 32) (1 + (2^r - 1)), the first factor from a
 // table of 32 values in two parts and the second's excess from four terms of its series
-// (the fifth is below 4e-13).
+// (the fifth is below 4e-13). The mantissa is put together as an integer and shifted.
+// kExact: l - m needs no second part (bf16 logits: it is a float32).
+template <bool kExact>
 __device__ __forceinline__ unsigned long long weight_fix(float l, float m, Slope c, const float2* tab) {
   if (l == m) return 1ull << kFixBits;
-  const float d = __fsub_rn(l, m);  // l - m = d + e exactly
-  const float bb = __fsub_rn(d, l);
-  const float e = __fadd_rn(__fsub_rn(l, __fsub_rn(d, bb)), __fsub_rn(-m, bb));
+  const float d = __fsub_rn(l, m);
   const float x = __fmul_rn(d, c.hi);
   if (!(x > -46.f)) return 0;  // below half a unit (or l not finite)
-  const float lo = __fmaf_rn(d, c.hi, -x) + __fmaf_rn(d, c.lo, e * c.hi);
+  float lo = __fmaf_rn(d, c.hi, -x);
+  lo = __fmaf_rn(d, c.lo, lo);
+  if constexpr (!kExact) {  // l - m = d + e exactly
+    const float bb = __fsub_rn(d, l);
+    const float e = __fadd_rn(__fsub_rn(l, __fsub_rn(d, bb)), __fsub_rn(-m, bb));
+    lo = __fmaf_rn(e, c.hi, lo);
+  }
   const float nf = rintf(x * 32.f);
   const int n = static_cast<int>(nf);
   const float r = __fmaf_rn(nf, -0.03125f, x) + lo;
   const float q = r * (0.693147182f + r * (0.240226507f + r * (0.0555041087f + r * 0.00961812911f)));
   const float2 h = tab[n & 31];
-  const float scale = __uint_as_float(static_cast<uint32_t>((n >> 5) + kFixBits + 127) << 23);
-  return __float2ull_rn(h.x * scale) + __float2ll_rn(__fmaf_rn(h.x, q, h.y) * scale);
+  const int low = __float2int_rn(__fmaf_rn(h.x, q, h.y) * 68719476736.f);  // 2^36: below 2^31
+  const uint32_t mant = (__float_as_uint(h.x) & 0x7fffffu) | 0x800000u;
+  const unsigned long long M =
+      (static_cast<unsigned long long>(mant) << 21) + (static_cast<long long>(low) << 8);
+  const int s = -(n >> 5);
+  return s > 0 ? (M + (1ull << (s - 1))) >> s : M;
 }
 
 template <typename T>
@@ -78,6 +109,19 @@ __device__ __forceinline__ float load_logit(const T* p, int j) {
   return to_f32<T>(p[j]) + 0.f;  // -0 counts as 0
 }
 __device__ __forceinline__ bool usable(float l) { return l > -INFINITY; }  // neither -inf nor NaN
+
+// The smallest weight of at least mp (0: any).
+__device__ __forceinline__ unsigned long long least_weight(float mp) {
+  return mp > 0.f ? __float2ull_ru(fminf(mp, 1.f) * static_cast<float>(1ull << kFixBits)) : 0;
+}
+// floor(f sum) and ceil(f sum) for 0 <= f < 1, exactly (f's bits below 2^-64 aside).
+__device__ __forceinline__ unsigned long long floor_part(float f, unsigned long long sum) {
+  return __umul64hi(__float2ull_rz(f * 18446744073709551616.f), sum);
+}
+__device__ __forceinline__ unsigned long long ceil_part(float f, unsigned long long sum) {
+  const unsigned long long g = __float2ull_rz(f * 18446744073709551616.f);
+  return __umul64hi(g, sum) + (g * sum != 0 ? 1 : 0);
+}
 
 template <typename V>
 __device__ __forceinline__ V warp_incl(V v) {
@@ -118,6 +162,7 @@ struct SlowScratch {
 template <typename T, int THREADS>
 __device__ __noinline__ void slow_row(const SampleFilteredArgs& a, int row, const float2* tab, SlowScratch scr) {
   constexpr int kSfThreads = THREADS, kSfWarps = THREADS / 32;
+  constexpr bool kExact = sizeof(T) == 2;
   __shared__ uint32_t s_digit;
   __shared__ unsigned long long s_above;
   __shared__ int s_pick;
@@ -186,16 +231,15 @@ __device__ __noinline__ void slow_row(const SampleFilteredArgs& a, int row, cons
     unsigned long long s = 0;
     for (int j = t; j < V; j += kSfThreads) {
       const float l = load_logit(lr, j);
-      if (usable(l) && order_key(l) > bd.key) s += weight_fix(l, m, c, tab);
+      if (usable(l) && order_key(l) > bd.key) s += weight_fix<kExact>(l, m, c, tab);
     }
     s = block_sum_u64<THREADS>(s, red);
-    if (bd.ties != INT_MAX && bd.key != 0) s += static_cast<unsigned long long>(bd.ties) * weight_fix(key_value(bd.key), m, c, tab);
+    if (bd.ties != INT_MAX && bd.key != 0) s += static_cast<unsigned long long>(bd.ties) * weight_fix<kExact>(key_value(bd.key), m, c, tab);
     return s;
   };
   if (p < 1.f) {
     const unsigned long long all = mass_of(border);
-    const double want = p > 0.f ? ceil(static_cast<double>(p) * static_cast<double>(all)) : 1.0;
-    unsigned long long left = min(all, max(1ull, static_cast<unsigned long long>(want)));
+    unsigned long long left = min(all, max(1ull, p > 0.f ? ceil_part(p, all) : 0ull));
     uint32_t prefix = 0;
     for (int shift = 24; shift >= 0; shift -= 8) {
       for (int i = t; i < 256; i += THREADS) hist[i] = 0;
@@ -205,7 +249,7 @@ __device__ __noinline__ void slow_row(const SampleFilteredArgs& a, int row, cons
         const float l = load_logit(lr, j);
         const uint32_t key = order_key(l);
         if (usable(l) && (key & mask) == prefix) {
-          const unsigned long long w = weight_fix(l, m, c, tab);
+          const unsigned long long w = weight_fix<kExact>(l, m, c, tab);
           if (w) atomicAdd(&hist[(key >> shift) & 255], w);
         }
       }
@@ -222,14 +266,13 @@ __device__ __noinline__ void slow_row(const SampleFilteredArgs& a, int row, cons
       left -= s_above;
       __syncthreads();
     }
-    const unsigned long long w = weight_fix(key_value(prefix), m, c, tab);
+    const unsigned long long w = weight_fix<kExact>(key_value(prefix), m, c, tab);
     const unsigned long long n = w ? (left + w - 1) / w : 1;
     int ties = static_cast<int>(min(n, static_cast<unsigned long long>(INT_MAX - 1)));
     if (prefix == border.key) ties = min(ties, border.ties);
     border = Border{prefix, ties};
   }
-  const unsigned long long least =
-      mp > 0.f ? static_cast<unsigned long long>(ceil(static_cast<double>(fminf(mp, 1.f)) * (1ull << kFixBits))) : 0;
+  const unsigned long long least = least_weight(mp);
 
   // Index order: each warp takes a contiguous share of the row; first the shares' ties
   // (those at the border's key are kept lowest index first), then their kept mass, then
@@ -263,7 +306,7 @@ __device__ __noinline__ void slow_row(const SampleFilteredArgs& a, int row, cons
       keep = usable(l);
     }
     if (!keep) return 0;
-    const unsigned long long w = weight_fix(l, m, c, tab);
+    const unsigned long long w = weight_fix<kExact>(l, m, c, tab);
     return w >= least ? w : 0;
   };
   unsigned long long mine = 0;
@@ -280,7 +323,7 @@ __device__ __noinline__ void slow_row(const SampleFilteredArgs& a, int row, cons
     if (w < warp) before += red[w];
     total += red[w];
   }
-  const unsigned long long draw = static_cast<unsigned long long>(static_cast<double>(u) * static_cast<double>(total));
+  const unsigned long long draw = floor_part(u, total);
   if (before <= draw && draw < before + mine) {
     unsigned long long at = before;
     int s2 = ties_before;
@@ -347,6 +390,18 @@ __device__ __forceinline__ void row_sync(int C) {  // every CTA of the row's clu
   }
 }
 
+// The largest of 16 bytes of logits (NaN aside).
+template <typename T>
+__device__ __forceinline__ float largest(const uint4& v) {
+  if constexpr (sizeof(T) == 4) {
+    return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)), fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
+  } else {
+    auto h = [](uint32_t x) { return *reinterpret_cast<const __nv_bfloat162*>(&x); };
+    const __nv_bfloat162 a = __hmax2(__hmax2(h(v.x), h(v.y)), __hmax2(h(v.z), h(v.w)));
+    return fmaxf(__low2float(a), __high2float(a));
+  }
+}
+
 // The first CTA's verdict, in every CTA's shared memory.
 struct Verdict {
   uint32_t status;  // kDrawn, kWalk, kEarlier, kLater, kTopKDone
@@ -376,10 +431,21 @@ struct RowSmem {
 
 // Sorts ent[0 .. n) descending, n a power of two (64 at least), by a bitonic network; exchanges
 // at distances up to 32 stay within a warp's 64 entries.
+// A list of at most one entry per thread is sorted by counting the larger entries instead.
 template <int THREADS>
-__device__ __forceinline__ void sort_entries(unsigned long long* ent, int n) {
+__device__ __forceinline__ void sort_entries(unsigned long long* ent, int n, int used) {
   const int t = threadIdx.x;
   __syncthreads();
+  if (used <= THREADS) {
+    const unsigned long long mine = t < used ? ent[t] : 0;
+    int above = 0;
+    if ((t & ~31) < used)
+      for (int i = 0; i < used; ++i) above += ent[i] > mine;
+    __syncthreads();
+    if (t < used) ent[above] = mine;
+    __syncthreads();
+    return;
+  }
   for (int k = 2; k <= n; k <<= 1) {
     for (int j = k >> 1; j > 0; j >>= 1) {
       for (int p = t; p < n / 2; p += THREADS) {
@@ -414,6 +480,7 @@ __device__ __forceinline__ void scan_values(unsigned long long (&v)[E], unsigned
 template <typename T, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kernel(const SampleFilteredArgs a, int C, int slice) {
   constexpr int NW = THREADS / 32, E = kList / THREADS, VEC = 16 / sizeof(T);
+  constexpr bool kExact = sizeof(T) == 2;
   extern __shared__ __align__(16) uint8_t row_raw[];
   T* sl = reinterpret_cast<T*>(row_raw);
   __shared__ RowSmem<THREADS> S;
@@ -421,11 +488,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
   // a peer's shared memory may be written only once the peer runs
   if (C > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  if (t < 32) {
-    const double h = exp2(t / 32.0);
-    S.tab[t].x = static_cast<float>(h);
-    S.tab[t].y = static_cast<float>(h - static_cast<double>(S.tab[t].x));
-  }
+  if (t < 32) S.tab[t] = kPowers[t];
   pdl_wait();
   const int rank = C > 1 ? static_cast<int>(cluster_rank()) : 0;
   const int row = blockIdx.x / C, b = row / a.per, V = a.V;
@@ -453,12 +516,9 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
       const uint32_t x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        if constexpr (sizeof(T) == 4) {
-          mx[e] = fmaxf(mx[e], __uint_as_float(x[e]));
-        } else {
-          mx[e] = fmaxf(mx[e], fmaxf(__uint_as_float(x[e] << 16), __uint_as_float(x[e] & 0xffff0000u)));
-        }
+        if constexpr (sizeof(T) == 4) mx[e] = fmaxf(mx[e], __uint_as_float(x[e]));
       }
+      if constexpr (sizeof(T) == 2) mx[0] = fmaxf(mx[0], largest<T>(v));
     }
     mine = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
   }
@@ -531,8 +591,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
   const float per = c.hi * kPerOctave;
   // place of a logit in units of bins, 0 at the largest; NaN and what has no weight at the end
   auto place = [&](float l) { return l == m ? 0.f : fminf(__fmul_rn(__fsub_rn(m, l), per), 511.5f); };
-  const unsigned long long least =
-      mp > 0.f ? static_cast<unsigned long long>(ceil(static_cast<double>(fminf(mp, 1.f)) * (1ull << kFixBits))) : 0;
+  const unsigned long long least = least_weight(mp);
 
   // ---- where the borders lie
   const bool by_count = k < V, by_mass = p < 1.f;
@@ -545,13 +604,17 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
   float base_mass = 0.f, shift_mass = 0.f;  // mass before the window; a correction once it is known exactly
   int lim = kTopBins;                  // bins counted so far
 
+  // A logit below this has a place past `y` (a little below it: places are rounded).
+  auto logit_at = [&](float y) { return m - (y + 0.01f) / per * 1.00001f - fabsf(m) * 1e-6f; };
   // Counts the bins of the window from `b0` up to `b1`; in the first window, also the masses
   // of its top bins and, when asked, the whole slice's mass.
   auto count_bins = [&](int b0, int b1, bool want_mass) {
     unsigned long long sum = 0;
     float low = 0.f;
+    const float cut = logit_at(x0 + b1 / scale);
     for (int i = t * VEC; i < slice; i += THREADS * VEC) {
       const uint4 v = *reinterpret_cast<const uint4*>(sl + i);
+      if (!want_mass && largest<T>(v) < cut) continue;
       const uint32_t x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
@@ -562,7 +625,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
           const int bin = static_cast<int>(y);
           atomicAdd(&S.cnt[bin], 1u);
           if (scale == 1.f && bin < kTopBins) {
-            const unsigned long long w = weight_fix(l, m, c, S.tab);
+            const unsigned long long w = weight_fix<kExact>(l, m, c, S.tab);
             atomicAdd(&S.mass[bin], w);
             sum += w;
           }
@@ -637,7 +700,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
     __syncthreads();
     return static_cast<int>(S.s_bin);
   };
-  auto goal_of = [&]() { return static_cast<float>(p * (static_cast<double>(whole) / (1ull << kFixBits))); };
+  auto goal_of = [&]() { return p * (static_cast<float>(whole) * (1.f / (1ull << kFixBits))); };
 
   // Back to the first window, all of its bins counted anew.
   auto first_window = [&]() {
@@ -734,8 +797,10 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
     __syncthreads();
     const int seg_len = slice / NW;
     unsigned long long kept = 0, all = 0;
+    const float cut = logit_at(fminf(xb, kLastBin));
     for (int i = warp * seg_len + lane * VEC; i < (warp + 1) * seg_len; i += 32 * VEC) {
       const uint4 q = *reinterpret_cast<const uint4*>(sl + i);
+      if (largest<T>(q) < cut) continue;
       const uint32_t x[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
@@ -744,7 +809,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
         const float pl = place(l);
         if (pl >= xb || pl >= kLastBin) continue;
         if (pl < xa) {
-          const unsigned long long w = weight_fix(l, m, c, S.tab);
+          const unsigned long long w = weight_fix<kExact>(l, m, c, S.tab);
           all += w;
           if (w >= least) kept += w;
         } else {
@@ -809,13 +874,13 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
         }
       }
       if (early && C > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // lists read
-      sort_entries<THREADS>(S.ent, n2);
+      sort_entries<THREADS>(S.ent, n2, N);
       // entry t E + e: its weight, and the weights up to and including it
       unsigned long long w[E], incl[E];
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         const int i = t * E + e;
-        w[e] = incl[e] = i < N ? weight_fix(key_value(static_cast<uint32_t>(S.ent[i] >> 32)), m, c, S.tab) : 0;
+        w[e] = incl[e] = i < N ? weight_fix<kExact>(key_value(static_cast<uint32_t>(S.ent[i] >> 32)), m, c, S.tab) : 0;
       }
       scan_values<E, THREADS>(incl, S.red);
       // the sum over the first x entries (x >= 1)
@@ -854,8 +919,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
         total = above + (keep ? upto(keep) : 0);
       }
       if (by_mass) {
-        const double want = p > 0.f ? ceil(static_cast<double>(p) * static_cast<double>(total)) : 1.0;
-        const unsigned long long goal = min(total, max(1ull, static_cast<unsigned long long>(want)));
+        const unsigned long long goal = min(total, max(1ull, p > 0.f ? ceil_part(p, total) : 0ull));
         if (count_left && !listed_only) {
           v.status = kTopKDone;  // top-p's border has still to be looked for, in another list
           v.total_lo = static_cast<uint32_t>(total);
@@ -887,8 +951,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
 #pragma unroll
           for (int e = 0; e < E; ++e) sum += t * E + e < keep && w[e] >= least ? w[e] : 0;
           sum = block_sum_u64<THREADS>(sum, S.red);
-          const unsigned long long draw =
-              static_cast<unsigned long long>(static_cast<double>(u) * static_cast<double>(sum));
+          const unsigned long long draw = floor_part(u, sum);
           int k2 = 64;
           while (k2 < keep) k2 *= 2;
           unsigned long long x[E];
@@ -901,11 +964,11 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
 #pragma unroll
           for (int e = 0; e < E; ++e)
             if (t * E + e < k2) S.ent[t * E + e] = x[e];
-          sort_entries<THREADS>(S.ent, k2);
+          sort_entries<THREADS>(S.ent, k2, keep);
 #pragma unroll
           for (int e = 0; e < E; ++e) {
             const int i = t * E + e;
-            w[e] = i < keep ? weight_fix(key_value(static_cast<uint32_t>(S.ent[i])), m, c, S.tab) : 0;
+            w[e] = i < keep ? weight_fix<kExact>(key_value(static_cast<uint32_t>(S.ent[i])), m, c, S.tab) : 0;
             if (w[e] < least) w[e] = 0;
             incl[e] = w[e];
           }
@@ -933,8 +996,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
             for (int i = 0; i < Q; ++i) s += own4[i] = lane * Q + i < C * NW ? S.all[lane * Q + i] : 0;
             const unsigned long long in = warp_incl(s);
             const unsigned long long tot = __shfl_sync(0xffffffffu, in, 31);
-            const unsigned long long draw =
-                static_cast<unsigned long long>(static_cast<double>(u) * static_cast<double>(tot));
+            const unsigned long long draw = floor_part(u, tot);
             const unsigned who = __ballot_sync(0xffffffffu, in > draw);
             if (lane == (who ? __ffs(who) - 1 : 31)) {
               unsigned long long before = in - s;
@@ -994,7 +1056,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
     const unsigned long long known = (static_cast<unsigned long long>(v.above_hi) << 32) | v.above_lo;
     const int lo = static_cast<int>((xa - x0) * scale), hi = static_cast<int>((xb - x0) * scale);
     const int edge = v.status == kLater ? hi : lo;
-    const float delta = static_cast<float>(static_cast<double>(known) / (1ull << kFixBits)) -
+    const float delta = static_cast<float>(known) * (1.f / (1ull << kFixBits)) -
                         (edge > 0 ? S.cm[edge - 1] : base_mass + shift_mass);
     shift_mass = scale == 1.f ? shift_mass + delta : delta;
     if (scale != 1.f && (v.status == kLater ? hi > kBins - 1 : lo < 1)) {  // outside the window
@@ -1028,7 +1090,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
       const uint32_t key = order_key(l);
       if (!(key > v.key || (key == v.key && static_cast<uint32_t>(j0 + i) <= v.tie_limit))) return 0;
     }
-    const unsigned long long w = weight_fix(l, m, c, S.tab);
+    const unsigned long long w = weight_fix<kExact>(l, m, c, S.tab);
     return w >= least ? w : 0;
   };
   unsigned long long sum = 0;
