@@ -11,13 +11,17 @@
 // 64 bits in whatever order.
 //
 // A row is held in the shared memory of a cluster of CTAs, so that it is read from memory
-// once. Its entries are sorted into bins by x = (m - l) * 11 log2(e) / T, eleven bins per
-// factor of two in weight; counts and masses of the bins say in which bins a border must
-// lie. Entries of lower x are kept whatever the border's exact place, so only their weights
-// are summed; the entries of the border's bins (at most kList) go to the first CTA, which
-// sorts them to find the exact border and then the draw: among the listed
-// entries when nothing else is kept, else in one of the row's segments, whose warp walks it.
-// A border among more than kList equal logits takes a slower path over the row in memory.
+// once. Its entries are counted in bins of x = (m - l) * 11 log2(e) / T, eleven bins per
+// factor of two in weight; counts and masses of the bins say in which bin a border must lie.
+// Entries of lower x are kept wherever in that bin the border is, so only their weights are
+// summed, per warp's segment of the row; the bin's own entries (a finer bin's where they are
+// more than kList) go to the first CTA, which sorts them, finds the exact border and the
+// segment in which the draw falls (or the draw itself where the list starts at the top). That
+// segment's CTA walks it. Equal logits need no list: the border is a number of them.
+//
+// The passes over the row are bound by instructions (a row of 152k logits is 4.7k per warp
+// and instruction), so each is kept to what its row needs: a top-k row looks at few entries
+// twice, top-p adds an exponential each. Decisions are the first CTA's alone.
 
 #include <algorithm>
 #include <climits>
@@ -351,11 +355,11 @@ __device__ __noinline__ void slow_row(const SampleFilteredArgs& a, int row, cons
 
 // ------------------------------------------------------------------ the cluster's row
 
-constexpr int kList = 1024;      // entries the first CTA can take
-constexpr int kBins = 512;       // bins of one window
+constexpr int kList = 256;          // entries the first CTA sorts
+constexpr int kBins = 512;          // bins of one window
 constexpr float kPerOctave = 11.f;  // 46 octaves (weights down to 2^-46) in 506 bins
-constexpr int kTopBins = 88;     // bins whose masses are exact (8 octaves); bins below: counted only
-constexpr int kLastBin = 507;    // from here on weights are 0
+constexpr int kTopBins = 88;        // bins (8 octaves) with exact weights; below, ex2's 2^-22 will do
+constexpr int kLastBin = 507;       // from here on weights are 0
 constexpr int kMaxCluster = 8;
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -381,13 +385,18 @@ __device__ __forceinline__ unsigned long long peer_load(const unsigned long long
 __device__ __forceinline__ void peer_store(uint32_t* p, uint32_t rank, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(peer(p, rank)), "r"(v) : "memory");
 }
-__device__ __forceinline__ void row_sync(int C) {  // every CTA of the row's cluster
-  if (C > 1) {
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+__device__ __forceinline__ void row_arrive(int C) {
+  if (C > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void row_wait(int C) {
+  if (C > 1)
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-  } else {
+  else
     __syncthreads();
-  }
+}
+__device__ __forceinline__ void row_sync(int C) {  // every CTA of the row's cluster
+  row_arrive(C);
+  row_wait(C);
 }
 
 // The largest of 16 bytes of logits (NaN aside).
@@ -401,85 +410,51 @@ __device__ __forceinline__ float largest(const uint4& v) {
     return fmaxf(__low2float(a), __high2float(a));
   }
 }
+// Logit e of 16 bytes of them; -0 becomes 0.
+template <typename T>
+__device__ __forceinline__ float logit_of(const uint4& v, int e) {
+  const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+  return (sizeof(T) == 4 ? __uint_as_float(x[e & 3])
+                         : __uint_as_float(e & 1 ? x[e >> 1] & 0xffff0000u : x[e >> 1] << 16)) + 0.f;
+}
 
-// The first CTA's verdict, in every CTA's shared memory.
-struct Verdict {
-  uint32_t status;  // kDrawn, kWalk, kEarlier, kLater, kTopKDone
-  uint32_t key, tie_limit;  // kept: larger keys, and this key up to this index
-  uint32_t segment;         // where the draw lies
-  uint32_t rem_lo, rem_hi, total_lo, total_hi, above_lo, above_hi;
+// What every CTA of a row does next, decided by the first one.
+enum : uint32_t { kDone = 0, kCount = 1, kPass = 2, kWalk = 3, kSlow = 4 };
+struct Command {
+  uint32_t what;
+  uint32_t fresh;         // kCount: in a new window, its bins zeroed first
+  int32_t b0, b1;         // kCount: which bins
+  float x0, scale;        // the window: bin = (x - x0) scale
+  float xa, xb;           // kPass: x < xa is kept, xa <= x < xb listed (or, ties, counted)
+  uint32_t early, ties;   // kPass: the first CTA goes on alone; the zone holds equal logits
+  uint32_t key, tie_limit;  // kWalk: kept of the zone: larger keys, and this key up to this index
+  uint32_t segment, tie_keep;  // kWalk: the draw's segment; ties: how many of them it keeps
+  uint32_t rem_lo, rem_hi, total_lo, total_hi;  // the draw's place in the segment, the kept mass
 };
-enum : uint32_t { kDrawn = 0, kWalk = 1, kEarlier = 2, kLater = 3, kTopKDone = 4 };
 
 template <int THREADS>
 struct RowSmem {
   float2 tab[32];
-  uint32_t cnt[kBins];                 // this CTA's counts in the window's bins
-  unsigned long long mass[kTopBins];   // and masses of the top bins
-  uint32_t cc[kBins];                  // the row's counts up to and including a bin
-  float cm[kBins];                     // and masses (estimated from the counts below the top bins)
-  unsigned long long ent[kList];       // listed entries: order_key << 32 | ~index
+  uint32_t cnt[kBins];                // this CTA's counts in the window's bins
+  unsigned long long mass[kTopBins];  // and masses of the top bins
+  uint32_t cc[kBins];                 // first CTA: the row's counts up to and including a bin
+  float cm[kBins];                    // and masses (estimated from the counts below the top bins)
+  unsigned long long ent[kList];      // listed entries: order_key << 32 | ~index
+  unsigned long long sorted[kList];
   unsigned long long red[32], seg[THREADS / 32], all[kMaxCluster * (THREADS / 32)];
-  unsigned long long own[2];           // this CTA's sum; its kept-whatever-the-border sum
-  uint32_t found[kMaxCluster];         // listed entries per CTA
-  uint32_t top[kMaxCluster];           // largest logits per CTA (bits)
-  uint32_t n_list, pick, s_bin;
+  unsigned long long own[2];          // this CTA's mass; its mass of x < xa
+  uint32_t segties[THREADS / 32], allties[kMaxCluster * (THREADS / 32)];
+  uint32_t found[kMaxCluster], key_min[kMaxCluster], key_max[kMaxCluster];  // listed entries per CTA, ...
+  uint32_t top[kMaxCluster];          // largest logits per CTA (bits)
+  uint32_t n_list, kmin, kmax, pick, tie_at;
   unsigned long long left, pickw;
-  int ties[32];
-  Verdict v;
+  int ties[32], bin;
+  Command cmd;
 };
-
-// Sorts ent[0 .. n) descending, n a power of two (64 at least), by a bitonic network; exchanges
-// at distances up to 32 stay within a warp's 64 entries.
-// A list of at most one entry per thread is sorted by counting the larger entries instead.
-template <int THREADS>
-__device__ __forceinline__ void sort_entries(unsigned long long* ent, int n, int used) {
-  const int t = threadIdx.x;
-  __syncthreads();
-  if (used <= THREADS) {
-    const unsigned long long mine = t < used ? ent[t] : 0;
-    int above = 0;
-    if ((t & ~31) < used)
-      for (int i = 0; i < used; ++i) above += ent[i] > mine;
-    __syncthreads();
-    if (t < used) ent[above] = mine;
-    __syncthreads();
-    return;
-  }
-  for (int k = 2; k <= n; k <<= 1) {
-    for (int j = k >> 1; j > 0; j >>= 1) {
-      for (int p = t; p < n / 2; p += THREADS) {
-        const int i = 2 * p - (p & (j - 1)), o = i + j;
-        const unsigned long long x = ent[i], y = ent[o];
-        if ((x < y) == ((i & k) == 0)) {
-          ent[i] = y;
-          ent[o] = x;
-        }
-      }
-      if (j > 32 || (j == 1 && k >= 64)) __syncthreads(); else __syncwarp();
-    }
-  }
-  __syncthreads();
-}
-
-// Inclusive sums over the block of E consecutive values per thread, in place.
-template <int E, int THREADS>
-__device__ __forceinline__ void scan_values(unsigned long long (&v)[E], unsigned long long* red) {
-#pragma unroll
-  for (int e = 1; e < E; ++e) v[e] += v[e - 1];
-  const unsigned long long incl = warp_incl(v[E - 1]);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 31) red[threadIdx.x >> 5] = incl;
-  __syncthreads();
-  unsigned long long before = incl - v[E - 1];
-  for (int w = 0; w < static_cast<int>(threadIdx.x >> 5); ++w) before += red[w];
-#pragma unroll
-  for (int e = 0; e < E; ++e) v[e] += before;
-}
 
 template <typename T, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kernel(const SampleFilteredArgs a, int C, int slice) {
-  constexpr int NW = THREADS / 32, E = kList / THREADS, VEC = 16 / sizeof(T);
+  constexpr int NW = THREADS / 32, VEC = 16 / sizeof(T);
   constexpr bool kExact = sizeof(T) == 2;
   extern __shared__ __align__(16) uint8_t row_raw[];
   T* sl = reinterpret_cast<T*>(row_raw);
@@ -508,19 +483,12 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
   int done = 0;
   if ((reinterpret_cast<uintptr_t>(lr) & 15) == 0) {
     done = n / VEC * VEC;
-    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 4
     for (int i = t * VEC; i < done; i += THREADS * VEC) {
       const uint4 v = __ldcs(reinterpret_cast<const uint4*>(src + i));
       *reinterpret_cast<uint4*>(sl + i) = v;
-      const uint32_t x[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if constexpr (sizeof(T) == 4) mx[e] = fmaxf(mx[e], __uint_as_float(x[e]));
-      }
-      if constexpr (sizeof(T) == 2) mx[0] = fmaxf(mx[0], largest<T>(v));
+      mine = fmaxf(mine, largest<T>(v));
     }
-    mine = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
   }
   for (int i = done + t; i < n; i += THREADS) {
     const T v = src[i];
@@ -566,14 +534,13 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
     if (rank == 0 && t == 0) emit(0, 0.f);
     return;
   }
-  auto at = [&](int i) { return to_f32<T>(sl[i]) + 0.f; };
   if (greedy) {  // the first CTA that holds the largest logit finds its lowest index
     int owner = 0;
     while (__uint_as_float(S.top[owner]) != m) ++owner;
     if (rank != owner) return;
     int best = INT_MAX;
     for (int i = t; i < n; i += THREADS)
-      if (at(i) == m) {
+      if (to_f32<T>(sl[i]) == m) {
         best = i;
         break;
       }
@@ -591,50 +558,59 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
   const float per = c.hi * kPerOctave;
   // place of a logit in units of bins, 0 at the largest; NaN and what has no weight at the end
   auto place = [&](float l) { return l == m ? 0.f : fminf(__fmul_rn(__fsub_rn(m, l), per), 511.5f); };
+  // a logit below this has a place past `y` (a little below it: places are rounded)
+  auto logit_at = [&](float y) { return m < INFINITY ? m - (y + 0.01f) / per * 1.00001f - fabsf(m) * 1e-6f : m; };
+  // the weight of a logit at place pl: far from the largest, by ex2 alone (its argument in two
+  // parts too: a slope off by one rounding would tilt the whole tail)
+  auto ex2_at = [&](float l, float shift) {
+    const float d = __fsub_rn(l, m);
+    float e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(__fmaf_rn(d, c.hi, __fmaf_rn(d, c.lo, shift))));
+    return e;
+  };
+  auto weight = [&](float l, float pl) -> unsigned long long {
+    if (pl < kTopBins) return weight_fix<kExact>(l, m, c, S.tab);
+    return pl < kLastBin ? __float2ull_rn(ex2_at(l, static_cast<float>(kFixBits))) : 0;
+  };
+  auto key_weight = [&](uint32_t key) {
+    const float l = key_value(key);
+    return weight(l, place(l));
+  };
+  auto ratio = [&](float l, unsigned long long sum) {  // the probability of a drawn logit
+    return static_cast<float>(static_cast<double>(weight_fix<kExact>(l, m, c, S.tab)) / static_cast<double>(sum));
+  };
   const unsigned long long least = least_weight(mp);
+  const bool by_count = k < V, by_mass = p < 1.f, by_mass_only = by_mass && !by_count;
+  const bool whole_list = V <= kList;
 
-  // ---- where the borders lie
-  const bool by_count = k < V, by_mass = p < 1.f;
-  unsigned long long whole = 0;  // the mass top-p takes its part of
-  float xa = INFINITY, xb = INFINITY;  // place < xa: kept whatever the border; xa <= place < xb: listed
-  uint32_t above_count = 0;            // entries of place < xa
-  bool count_left = by_count;          // top-k's border is still to be found
-  float x0 = 0.f, scale = 1.f;         // the window's bins: (place - x0) * scale
-  uint32_t base_count = 0;             // entries before the window
-  float base_mass = 0.f, shift_mass = 0.f;  // mass before the window; a correction once it is known exactly
-  int lim = kTopBins;                  // bins counted so far
-
-  // A logit below this has a place past `y` (a little below it: places are rounded).
-  auto logit_at = [&](float y) { return m - (y + 0.01f) / per * 1.00001f - fabsf(m) * 1e-6f; };
-  // Counts the bins of the window from `b0` up to `b1`; in the first window, also the masses
-  // of its top bins and, when asked, the whole slice's mass.
-  auto count_bins = [&](int b0, int b1, bool want_mass) {
+  // Counts the entries in bins b0 up to b1 of the window, and the masses of the top bins; for
+  // top-p alone also the slice's whole mass.
+  auto count_bins = [&](const Command& cmd, bool want_mass) {
     unsigned long long sum = 0;
     float low = 0.f;
-    const float cut = logit_at(x0 + b1 / scale);
+    const float x0 = cmd.x0, scale = cmd.scale, cut = logit_at(x0 + cmd.b1 / scale);
+    const bool first = scale == 1.f;
     for (int i = t * VEC; i < slice; i += THREADS * VEC) {
       const uint4 v = *reinterpret_cast<const uint4*>(sl + i);
       if (!want_mass && largest<T>(v) < cut) continue;
-      const uint32_t x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        const float l = (sizeof(T) == 4 ? __uint_as_float(x[e & 3])
-                                        : __uint_as_float(e & 1 ? x[e >> 1] & 0xffff0000u : x[e >> 1] << 16)) + 0.f;
-        const float pl = place(l), y = scale == 1.f ? pl : (pl - x0) * scale;
-        if (y >= b0 && y < b1) {
-          const int bin = static_cast<int>(y);
-          atomicAdd(&S.cnt[bin], 1u);
-          if (scale == 1.f && bin < kTopBins) {
-            const unsigned long long w = weight_fix<kExact>(l, m, c, S.tab);
-            atomicAdd(&S.mass[bin], w);
-            sum += w;
+        const float l = logit_of<T>(v, e);
+        float wf = want_mass ? fmaxf(ex2_at(l, 0.f), 0.f) : 0.f;  // NaN: nothing
+        if (l >= cut) {
+          const float pl = place(l), y = first ? pl : (pl - x0) * scale;
+          if (y >= cmd.b0 && y < cmd.b1) {
+            const int bin = static_cast<int>(y);
+            atomicAdd(&S.cnt[bin], 1u);
+            if (first && bin < kTopBins) {
+              const unsigned long long w = weight_fix<kExact>(l, m, c, S.tab);
+              atomicAdd(&S.mass[bin], w);
+              sum += w;
+              wf = 0.f;
+            }
           }
-        } else if (want_mass) {
-          const float d = __fsub_rn(l, m);
-          float wf;
-          asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(wf) : "f"(__fmaf_rn(d, c.hi, d * c.lo)));
-          low += wf > 0.f ? wf : 0.f;  // NaN: nothing
         }
+        low += wf;
       }
     }
     if (want_mass) {
@@ -643,9 +619,20 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
       if (t == 0) S.own[0] = sum;
     }
   };
-  // The row's running counts and masses over the window's bins.
-  auto total_bins = [&]() {
-    constexpr int PER = kBins / THREADS;  // 2 or 1
+
+  // ---- the first CTA's knowledge of the borders
+  unsigned long long whole = 0;        // the mass top-p takes its part of
+  bool count_left = by_count;          // top-k's border is still to be found
+  uint32_t above_count = 0;            // entries of x < xa
+  uint32_t base_count = 0;             // entries before the window
+  float base_mass = 0.f, shift = 0.f;  // mass before the window; what an exact sum has shown its estimate to lack
+  int first_least = 0, first_most = kBins - 1, at_least = 0, at_most = kBins - 1;  // bounds of the border's bin
+  int lim = 0;                         // bins of the first window counted so far
+
+  // The row's running counts and masses over the window's bins, into S.cc and S.cm.
+  auto total_bins = [&](const Command& cmd) {
+    constexpr int PER = kBins / THREADS;
+    const bool first = cmd.scale == 1.f;
     uint32_t cs[PER], csum = 0;
     float ms[PER], msum = 0.f;
 #pragma unroll
@@ -653,14 +640,12 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
       const int bin = t * PER + i;
       cs[i] = 0;
       ms[i] = 0.f;
-      if (bin < lim || scale != 1.f) {
+      if (bin < cmd.b1) {
         cs[i] = row_total(&S.cnt[bin]);
-        if (scale == 1.f && bin < kTopBins) {
-          const unsigned long long q = row_total(&S.mass[bin]);
-          ms[i] = static_cast<float>(q) * (1.f / (1ull << kFixBits));
-        } else {
-          ms[i] = cs[i] * exp2f(-(x0 + (bin + 0.5f) / scale) / kPerOctave);
-        }
+        if (first && bin < kTopBins)
+          ms[i] = static_cast<float>(row_total(&S.mass[bin])) * (1.f / (1ull << kFixBits));
+        else
+          ms[i] = cs[i] * exp2f(-(cmd.x0 + (bin + 0.5f) / cmd.scale) / kPerOctave);
       }
       csum += cs[i];
       msum += ms[i];
@@ -674,7 +659,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
     }
     __syncthreads();
     uint32_t cb = base_count + ci - csum;
-    float mb = base_mass + shift_mass + mi - msum;
+    float mb = base_mass + shift + mi - msum;
     for (int w = 0; w < warp; ++w) {
       cb += S.ties[w];
       mb += __uint_as_float(static_cast<uint32_t>(S.red[w]));
@@ -688,409 +673,434 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
     }
     __syncthreads();
   };
-  // The first bin that reaches `k` entries (count) or the mass `goal`; kBins: none.
-  auto border_bin = [&](bool count, float goal) {
-    if (t == 0) S.s_bin = kBins;
+  // The next command from the window's counts: a list around the border, more counting, or
+  // (too many entries in one bin) a window on the bin.
+  auto choose = [&](Command cmd) {
+    const bool first = cmd.scale == 1.f;
+    const int last = first ? lim - 1 : kBins - 1;
+    const float goal = p * (static_cast<float>(whole) * (1.f / (1ull << kFixBits)));
+    if (t == 0) S.bin = kBins;
     __syncthreads();
-    for (int i = t; i < kBins; i += THREADS) {
-      const bool here = count ? S.cc[i] >= static_cast<uint32_t>(k) : S.cm[i] >= goal;
-      const bool before = i > 0 && (count ? S.cc[i - 1] >= static_cast<uint32_t>(k) : S.cm[i - 1] >= goal);
-      if (here && !before) atomicMin(&S.s_bin, static_cast<uint32_t>(i));
+    for (int i = t; i <= last; i += THREADS) {
+      const bool here = count_left ? S.cc[i] >= static_cast<uint32_t>(k) : S.cm[i] >= goal;
+      const bool before = i > 0 && (count_left ? S.cc[i - 1] >= static_cast<uint32_t>(k) : S.cm[i - 1] >= goal);
+      if (here && !before) atomicMin(&S.bin, i);
     }
     __syncthreads();
-    return static_cast<int>(S.s_bin);
-  };
-  auto goal_of = [&]() { return p * (static_cast<float>(whole) * (1.f / (1ull << kFixBits))); };
-
-  // Back to the first window, all of its bins counted anew.
-  auto first_window = [&]() {
-    x0 = 0.f, scale = 1.f, base_count = 0, base_mass = 0.f, lim = kLastBin;
-    row_sync(C);  // the counts have been read
-    for (int i = t; i < kBins; i += THREADS) S.cnt[i] = 0;
-    if (t < kTopBins) S.mass[t] = 0;
+    int B = S.bin;
     __syncthreads();
-    count_bins(0, kLastBin, false);
-    row_sync(C);
-    total_bins();
-  };
-
-  bool slow = false;
-  // What earlier rounds have shown of the border's bin, in the first window and in a later one.
-  int first_least = 0, first_most = kBins - 1, at_least = 0, at_most = kBins - 1;
-  if (by_count || by_mass) {
-    if (V <= kList) {
-      xa = 0.f;
-      xb = kLastBin;
-      if (by_mass && !by_count) whole = ~0ull;  // summed from the list
-    } else {
-      count_bins(0, kTopBins, by_mass && !by_count);
-      row_sync(C);
-      if (by_mass && !by_count)
-        whole = row_total(&S.own[0]);
-      total_bins();
+    cmd.early = cmd.ties = cmd.fresh = 0;
+    if (B == kBins && first && lim < kLastBin) {  // below the bins counted so far
+      cmd.what = kCount;
+      cmd.b0 = lim;
+      cmd.b1 = lim = kLastBin;
+      return cmd;
     }
-  }
-  Verdict v{};
-  for (int round = 0;; ++round) {
-    // ---- choose the entries to list
-    if ((by_count || by_mass) && V > kList && !slow) {
-      for (;;) {
-        int B = border_bin(count_left, goal_of());
-        if (B == kBins && scale == 1.f && lim < kLastBin) {  // below the top bins: count the rest
-          row_sync(C);
-          count_bins(kTopBins, kLastBin, false);
-          lim = kLastBin;
-          row_sync(C);
-          total_bins();
-          continue;
-        }
-        if (B == kBins) B = scale == 1.f ? lim - 1 : kBins - 1;  // all that has weight, or a mass estimate too low
-        B = scale == 1.f ? max(first_least, min(B, first_most)) : max(at_least, min(B, at_most));
-        if (S.cc[B] <= kList) {  // everything down to the border fits
-          int hi = B;
-          if (!count_left && hi + 1 < (scale == 1.f ? lim : kBins) && S.cc[hi + 1] <= kList) ++hi;
-          xa = 0.f;
-          xb = x0 + (hi + 1) / scale;
-          above_count = 0;
-          break;
-        }
-        const uint32_t before = B ? S.cc[B - 1] : base_count;
-        if (S.cc[B] - before <= kList) {
-          int lo = B, hi = B;
-          if (!count_left) {  // the masses are estimates: list the neighbours too where they fit
-            const int last = scale == 1.f ? lim - 1 : kBins - 1;
-            if (lo > 0 && S.cc[hi] - (lo > 1 ? S.cc[lo - 2] : base_count) <= kList) --lo;
-            if (hi < last && S.cc[hi + 1] - (lo > 0 ? S.cc[lo - 1] : base_count) <= kList) ++hi;
-          }
-          xa = x0 + lo / scale;
-          xb = x0 + (hi + 1) / scale;
-          above_count = lo > 0 ? S.cc[lo - 1] : base_count;
-          break;
-        }
-        if (scale != 1.f) {  // more than kList within 2^(1/5632): equal logits
-          slow = true;
-          break;
-        }
-        // a window on the bin alone
-        base_mass = B ? S.cm[B - 1] : base_mass + shift_mass;
-        shift_mass = 0.f;
-        base_count = before;
-        x0 += B / scale;
-        scale *= kBins;
-        at_least = 0, at_most = kBins - 1;
-        row_sync(C);  // the counts have been read
-        for (int i = t; i < kBins; i += THREADS) S.cnt[i] = 0;
-        __syncthreads();
-        count_bins(0, kBins, false);
-        row_sync(C);
-        total_bins();
+    if (B == kBins) B = last;  // all that has weight, or a mass estimated too low
+    B = first ? max(first_least, min(B, first_most)) : max(at_least, min(B, at_most));
+    cmd.what = kPass;
+    const uint32_t before = B ? S.cc[B - 1] : base_count, here = S.cc[B] - before;
+    if (S.cc[B] <= kList) {  // everything down to the border fits
+      int hi = B;
+      if (!count_left && hi < last && S.cc[hi + 1] <= kList) ++hi;
+      cmd.xa = 0.f;
+      cmd.xb = cmd.x0 + (hi + 1) / cmd.scale;
+      above_count = 0;
+      cmd.early = count_left;  // top-k's border is there for certain; a mass is an estimate
+    } else if (here <= kList || !first) {
+      int lo = B, hi = B;
+      if (here > kList) {
+        cmd.ties = 1;  // within 2^(1/5632) of one another: equal logits
+      } else if (!count_left) {  // the masses are estimates: take the neighbours too where they fit
+        if (lo > 0 && S.cc[hi] - (lo > 1 ? S.cc[lo - 2] : base_count) <= kList) --lo;
+        if (hi < last && S.cc[hi + 1] - (lo > 0 ? S.cc[lo - 1] : base_count) <= kList) ++hi;
       }
-      if (slow) {
-        row_sync(C);  // peers have read this CTA's counts
-        if (rank == 0) slow_row<T, THREADS>(a, row, S.tab, SlowScratch{S.red, S.ent, S.ties});
+      cmd.xa = cmd.x0 + lo / cmd.scale;
+      cmd.xb = cmd.x0 + (hi + 1) / cmd.scale;
+      above_count = lo > 0 ? S.cc[lo - 1] : base_count;
+    } else {  // a window on the bin
+      base_mass = B ? S.cm[B - 1] : base_mass + shift;
+      shift = 0.f;
+      base_count = before;
+      at_least = 0, at_most = kBins - 1;
+      cmd.what = kCount;
+      cmd.fresh = 1;
+      cmd.x0 = static_cast<float>(B);
+      cmd.scale = kBins;
+      cmd.b0 = 0;
+      cmd.b1 = kBins;
+    }
+    return cmd;
+  };
+
+  Command cmd{};
+  cmd.scale = 1.f;
+  if (!by_count && !by_mass) {
+    cmd.what = kPass;
+    cmd.xa = cmd.xb = INFINITY;
+  } else if (whole_list) {
+    cmd.what = kPass;
+    cmd.xb = kLastBin;
+    cmd.early = 1;
+  } else {
+    cmd.what = kCount;
+    cmd.b1 = lim = by_mass_only ? kLastBin : kTopBins;
+  }
+  const int seg_len = slice / NW;
+  for (int round = 0;; ++round) {
+    if (cmd.what == kCount) {
+      if (cmd.fresh) {
+        for (int i = t; i < kBins; i += THREADS) S.cnt[i] = 0;
+        if (t < kTopBins) S.mass[t] = 0;
+        __syncthreads();
+      }
+      count_bins(cmd, by_mass_only && round == 0);
+      row_sync(C);
+      if (rank == 0) {
+        if (by_mass_only && round == 0) whole = row_total(&S.own[0]);
+        Command all = cmd;
+        all.b0 = 0;
+        total_bins(all);
+        cmd = choose(cmd);
+      }
+    } else {
+      // ---- one pass: sum what is kept anyhow (per warp's segment), list the rest
+      if (t == 0) S.n_list = 0, S.kmin = 0xffffffffu, S.kmax = 0;
+      __syncthreads();
+      unsigned long long kept = 0, all = 0;
+      uint32_t tied = 0, kmin = 0xffffffffu, kmax = 0;
+      const float xa = cmd.xa, xb = fminf(cmd.xb, kLastBin), cut = logit_at(xb);
+      for (int i = warp * seg_len + lane * VEC; i < (warp + 1) * seg_len; i += 32 * VEC) {
+        const uint4 q = *reinterpret_cast<const uint4*>(sl + i);
+        if (largest<T>(q) < cut) continue;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          const float l = logit_of<T>(q, e);
+          if (!(l >= cut)) continue;
+          const float pl = place(l);
+          if (pl >= xb) continue;
+          if (pl < xa) {
+            const unsigned long long w = weight(l, pl);
+            all += w;
+            if (w >= least) kept += w;
+          } else if (cmd.ties) {
+            const uint32_t key = order_key(l);
+            ++tied;
+            kmin = min(kmin, key);
+            kmax = max(kmax, key);
+          } else {
+            const uint32_t pos = atomicAdd(&S.n_list, 1u);
+            if (pos < kList)
+              S.ent[pos] = (static_cast<unsigned long long>(order_key(l)) << 32) | ~static_cast<uint32_t>(j0 + i + e);
+          }
+        }
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        kept += __shfl_xor_sync(0xffffffffu, kept, o);
+        all += __shfl_xor_sync(0xffffffffu, all, o);
+        tied += __shfl_xor_sync(0xffffffffu, tied, o);
+      }
+      if (cmd.ties && kmax) {
+        atomicMin(&S.kmin, kmin);
+        atomicMax(&S.kmax, kmax);
+      }
+      if (lane == 0) {
+        S.seg[warp] = kept;
+        S.segties[warp] = tied;
+        S.red[warp] = all;
+      }
+      __syncthreads();
+      if (t == 0) {
+        unsigned long long s = 0;
+        for (int w = 0; w < NW; ++w) s += S.red[w];
+        S.own[1] = s;
+      }
+      if (t < C) {
+        if (C > 1) {
+          peer_store(&S.found[rank], t, S.n_list);
+          peer_store(&S.key_min[rank], t, S.kmin);
+          peer_store(&S.key_max[rank], t, S.kmax);
+        } else {
+          S.found[0] = S.n_list, S.key_min[0] = S.kmin, S.key_max[0] = S.kmax;
+        }
+      }
+      row_sync(C);
+      const bool early = cmd.early;
+      if (early && rank != 0) {  // the first CTA goes on alone once it has read the lists
+        row_arrive(C);
+        row_wait(C);
         return;
       }
-    }
-
-    // ---- one pass: sum what is kept anyhow (per warp's segment), list the rest
-    if (t == 0) S.n_list = 0;
-    __syncthreads();
-    const int seg_len = slice / NW;
-    unsigned long long kept = 0, all = 0;
-    const float cut = logit_at(fminf(xb, kLastBin));
-    for (int i = warp * seg_len + lane * VEC; i < (warp + 1) * seg_len; i += 32 * VEC) {
-      const uint4 q = *reinterpret_cast<const uint4*>(sl + i);
-      if (largest<T>(q) < cut) continue;
-      const uint32_t x[4] = {q.x, q.y, q.z, q.w};
+      if (rank == 0) {
+        // ---- the border and the draw
+        const unsigned long long above = row_total(&S.own[1]);
+        uint32_t start[kMaxCluster + 1], lo_key = 0xffffffffu, hi_key = 0;
+        start[0] = 0;
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const float l = (sizeof(T) == 4 ? __uint_as_float(x[e & 3])
-                                        : __uint_as_float(e & 1 ? x[e >> 1] & 0xffff0000u : x[e >> 1] << 16)) + 0.f;
-        const float pl = place(l);
-        if (pl >= xb || pl >= kLastBin) continue;
-        if (pl < xa) {
-          const unsigned long long w = weight_fix<kExact>(l, m, c, S.tab);
-          all += w;
-          if (w >= least) kept += w;
-        } else {
-          const uint32_t pos = atomicAdd(&S.n_list, 1u);
-          if (pos < kList)
-            S.ent[pos] = (static_cast<unsigned long long>(order_key(l)) << 32) | ~static_cast<uint32_t>(j0 + i + e);
+        for (int r = 0; r < kMaxCluster; ++r) {
+          start[r + 1] = start[r] + (r < C ? S.found[r] : 0);
+          if (r < C) lo_key = min(lo_key, S.key_min[r]), hi_key = max(hi_key, S.key_max[r]);
         }
-      }
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      kept += __shfl_xor_sync(0xffffffffu, kept, o);
-      all += __shfl_xor_sync(0xffffffffu, all, o);
-    }
-    if (lane == 0) {
-      S.seg[warp] = kept;
-      S.red[warp] = all;
-    }
-    __syncthreads();
-    if (t == 0) {
-      unsigned long long s = 0;
-      for (int w = 0; w < NW; ++w) s += S.red[w];
-      S.own[1] = s;
-    }
-    if (t < C) {
-      if (C > 1)
-        peer_store(&S.found[rank], t, S.n_list);
-      else
-        S.found[0] = S.n_list;
-    }
-    row_sync(C);
-
-    // ---- the first CTA finds the border and the draw
-    const bool listed_only = xa == 0.f;
-    // a list from the top holds top-k's border for certain (a mass, estimated, may fall short
-    // of top-p's): the other CTAs are then no longer needed once it has been read
-    const bool early = listed_only && (V <= kList || count_left);
-    if (rank == 0) {
-      uint32_t start[kMaxCluster + 1];
-      start[0] = 0;
-#pragma unroll
-      for (int r = 0; r < kMaxCluster; ++r) start[r + 1] = start[r] + (r < C ? S.found[r] : 0);
-      const int N = static_cast<int>(min(start[kMaxCluster], static_cast<uint32_t>(kList)));
-      int n2 = 64;
-      while (n2 < N) n2 *= 2;
-      unsigned long long above = row_total(&S.own[1]);
-      {
-        unsigned long long got[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const uint32_t i = t + e * THREADS;
-          got[e] = 0;
-          if (i < start[1] || i >= static_cast<uint32_t>(N)) continue;  // this CTA's own lie in place
-          int r = 1;
-          while (r + 1 < C && i >= start[r + 1]) ++r;
-          got[e] = peer_load(&S.ent[i - start[r]], r);
+        const int N = static_cast<int>(min(start[kMaxCluster], static_cast<uint32_t>(kList)));
+        unsigned long long ent = 0;
+        if (t < N) {
+          int r = 0;
+          while (r + 1 < C && t >= static_cast<int>(start[r + 1])) ++r;
+          ent = C > 1 ? peer_load(&S.ent[t - start[r]], r) : S.ent[t];
         }
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const int i = t + e * THREADS;
-          if (i >= static_cast<int>(start[1]) && i < n2) S.ent[i] = got[e];
-        }
-      }
-      if (early && C > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // lists read
-      sort_entries<THREADS>(S.ent, n2, N);
-      // entry t E + e: its weight, and the weights up to and including it
-      unsigned long long w[E], incl[E];
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const int i = t * E + e;
-        w[e] = incl[e] = i < N ? weight_fix<kExact>(key_value(static_cast<uint32_t>(S.ent[i] >> 32)), m, c, S.tab) : 0;
-      }
-      scan_values<E, THREADS>(incl, S.red);
-      // the sum over the first x entries (x >= 1)
-      auto upto = [&](int x) {
-        if ((x - 1) / E == t) {
-#pragma unroll
-          for (int e = 0; e < E; ++e)
-            if ((x - 1) % E == e) S.left = incl[e];
+        if (cmd.ties)
+          for (int i = t; i < C * NW; i += THREADS)
+            S.allties[i] = C > 1 ? peer_load(&S.segties[i % NW], i / NW) : S.segties[i];
+        if (!early)
+          for (int i = t; i < C * NW; i += THREADS) S.all[i] = C > 1 ? peer_load(&S.seg[i % NW], i / NW) : S.seg[i];
+        if (early) row_arrive(C);  // lists read
+        __syncthreads();
+        // sorted by counting the larger entries
+        if (t < N) S.ent[t] = ent;
+        __syncthreads();
+        if (t < N) {
+          int larger = 0;
+          for (int i = 0; i < N; ++i) larger += S.ent[i] > ent;
+          S.sorted[larger] = ent;
         }
         __syncthreads();
-        const unsigned long long s = S.left;
-        __syncthreads();
-        return s;
-      };
-      // how many leading entries satisfy a condition that once false stays false
-      auto leading = [&](auto cond) {
-        int x = 0;
-#pragma unroll
-        for (int e = 0; e < E; ++e) x += t * E + e < N && cond(w[e], incl[e]) ? 1 : 0;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-        if (lane == 0) S.ties[warp] = x;
-        __syncthreads();
-        x = 0;
-        for (int q = 0; q < NW; ++q) x += S.ties[q];
-        __syncthreads();
-        return x;
-      };
-      v = Verdict{kDrawn, 0u, 0xffffffffu, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-      const unsigned long long zone = N ? upto(N) : 0;
-      unsigned long long total = by_mass && !by_count && V <= kList ? zone : whole;
-      int keep = N;  // the first so many entries are kept
-      if (count_left) {
-        const uint32_t want = k - above_count;
-        if (want < static_cast<uint32_t>(N)) keep = want;
-        total = above + (keep ? upto(keep) : 0);
-      }
-      if (by_mass) {
-        const unsigned long long goal = min(total, max(1ull, p > 0.f ? ceil_part(p, total) : 0ull));
-        if (count_left && !listed_only) {
-          v.status = kTopKDone;  // top-p's border has still to be looked for, in another list
-          v.total_lo = static_cast<uint32_t>(total);
-          v.total_hi = static_cast<uint32_t>(total >> 32);
-        } else if (goal <= above) {
-          v.status = kEarlier;
-        } else if (goal - above > zone && xb < kLastBin) {
-          v.status = kLater;
-          above += zone;  // up to the list's end
-        } else {
-          const unsigned long long rest = goal - above;
-          keep = min(keep, leading([&](unsigned long long wi, unsigned long long in) { return in - wi < rest; }));
-        }
-        v.above_lo = static_cast<uint32_t>(above);
-        v.above_hi = static_cast<uint32_t>(above >> 32);
-      }
-      if (v.status == kDrawn) {
-        // min-p is asked of each entry, here as in the walk below
-        if (keep > 0) {
-          v.key = static_cast<uint32_t>(S.ent[keep - 1] >> 32);
-          v.tie_limit = ~static_cast<uint32_t>(S.ent[keep - 1]);
-        } else {
-          v.key = 0xffffffffu;  // none of the list
-          v.tie_limit = 0;
-        }
-        if (listed_only) {
-          // the kept entries in index order: the draw is the first whose sum passes it
-          unsigned long long sum = 0;
-#pragma unroll
-          for (int e = 0; e < E; ++e) sum += t * E + e < keep && w[e] >= least ? w[e] : 0;
-          sum = block_sum_u64<THREADS>(sum, S.red);
-          const unsigned long long draw = floor_part(u, sum);
-          int k2 = 64;
-          while (k2 < keep) k2 *= 2;
-          unsigned long long x[E];
-#pragma unroll
-          for (int e = 0; e < E; ++e) {
-            const int i = t * E + e;
-            x[e] = i < keep ? (S.ent[i] << 32) | (S.ent[i] >> 32) : 0;
-          }
+        // entry t in order: its weight, and the weights up to and including it
+        ent = t < N ? S.sorted[t] : 0;
+        const unsigned long long w = t < N ? key_weight(static_cast<uint32_t>(ent >> 32)) : 0;
+        auto scan = [&](unsigned long long v) {  // inclusive over the block
+          const unsigned long long in = warp_incl(v);
           __syncthreads();
-#pragma unroll
-          for (int e = 0; e < E; ++e)
-            if (t * E + e < k2) S.ent[t * E + e] = x[e];
-          sort_entries<THREADS>(S.ent, k2, keep);
-#pragma unroll
-          for (int e = 0; e < E; ++e) {
-            const int i = t * E + e;
-            w[e] = i < keep ? weight_fix<kExact>(key_value(static_cast<uint32_t>(S.ent[i])), m, c, S.tab) : 0;
-            if (w[e] < least) w[e] = 0;
-            incl[e] = w[e];
+          if (lane == 31) S.red[warp] = in;
+          __syncthreads();
+          unsigned long long before = 0;
+          for (int q = 0; q < warp; ++q) before += S.red[q];
+          return in + before;
+        };
+        const unsigned long long incl = scan(w);
+        if (t == max(N, 1) - 1) S.left = incl;
+        __syncthreads();
+        unsigned long long zone = S.left;
+        uint32_t in_zone = N;
+        unsigned long long tie_w = 0;
+        bool slow = round >= 64;
+        if (cmd.ties) {
+          in_zone = 0;
+          for (int i = 0; i < C * NW; ++i) in_zone += S.allties[i];
+          if (lo_key != hi_key) slow = true;  // not equal after all
+          tie_w = key_weight(hi_key);
+          zone = in_zone * tie_w;
+        }
+        // the mass of the first x of the zone
+        auto upto = [&](uint32_t x) {
+          if (cmd.ties) return x * tie_w;
+          __syncthreads();
+          if (t == static_cast<int>(x) - 1) S.left = incl;
+          __syncthreads();
+          return x ? S.left : 0ull;
+        };
+        uint32_t keep = in_zone;
+        unsigned long long total = by_mass_only && whole_list ? zone : whole;
+        if (count_left) {
+          keep = min(in_zone, k - above_count);
+          total = above + upto(keep);
+        }
+        const bool from_top = cmd.xa == 0.f && !cmd.ties;
+        int again = 0;  // -1, 1: the border lies before or behind the zone; 2: top-p's border is next
+        if (by_mass) {
+          const unsigned long long goal = min(total, max(1ull, p > 0.f ? ceil_part(p, total) : 0ull));
+          if (count_left && !from_top) {
+            again = 2;
+            whole = total;
+            count_left = false;
+          } else if (goal <= above) {
+            again = -1;
+          } else if (goal - above > zone && cmd.xb < kLastBin) {
+            again = 1;
+          } else {
+            const unsigned long long rest = goal - above;
+            uint32_t take;
+            if (cmd.ties)
+              take = tie_w ? static_cast<uint32_t>(min((rest + tie_w - 1) / tie_w, 0xffffffffull)) : 1;
+            else
+              take = __syncthreads_count(t < N && incl - w < rest);
+            keep = min(keep, take);
           }
-          scan_values<E, THREADS>(incl, S.red);
-#pragma unroll
-          for (int e = 0; e < E; ++e)
-            if (incl[e] > draw && incl[e] - w[e] <= draw)
-              emit(~static_cast<uint32_t>(S.ent[t * E + e] >> 32),
-                   static_cast<float>(static_cast<double>(w[e]) / static_cast<double>(sum)));
+        }
+        if (slow) {
+          cmd.what = kSlow;
+        } else if (again == 2) {
+          if (cmd.scale == 1.f) {
+            cmd = choose(cmd);
+          } else {  // back to the first window
+            cmd.what = kCount, cmd.fresh = 1, cmd.x0 = 0.f, cmd.scale = 1.f, cmd.b0 = 0, cmd.b1 = lim = kLastBin;
+            base_count = 0, base_mass = 0.f;
+          }
+        } else if (again) {
+          // a neighbouring bin, with the exact mass up to this list's start (or end) for its estimate
+          const int lo = static_cast<int>((cmd.xa - cmd.x0) * cmd.scale);
+          const int hi = static_cast<int>((cmd.xb - cmd.x0) * cmd.scale), edge = again > 0 ? hi : lo;
+          const unsigned long long known = again > 0 ? above + zone : above;
+          const float delta = static_cast<float>(known) * (1.f / (1ull << kFixBits)) -
+                              (edge > 0 ? S.cm[edge - 1] : base_mass + shift);
+          const bool first = cmd.scale == 1.f;
+          if (!first && (again > 0 ? hi > kBins - 1 : lo < 1)) {  // outside the window
+            if (again > 0)
+              first_least = static_cast<int>(cmd.x0) + 1;
+            else
+              first_most = static_cast<int>(cmd.x0) - 1;
+            shift = delta;
+            cmd.what = kCount, cmd.fresh = 1, cmd.x0 = 0.f, cmd.scale = 1.f, cmd.b0 = 0, cmd.b1 = lim = kLastBin;
+            base_count = 0, base_mass = 0.f;
+          } else {
+            if (again > 0)
+              (first ? first_least : at_least) = hi;
+            else
+              (first ? first_most : at_most) = lo - 1;
+            if (first) shift += delta; else base_mass += delta;
+            __syncthreads();
+            for (int i = t; i < kBins; i += THREADS) S.cm[i] += delta;
+            __syncthreads();
+            cmd = choose(cmd);
+          }
+        } else if (from_top) {
+          // the kept entries in index order: the draw is the first whose sum passes it
+          const uint32_t idx = ~static_cast<uint32_t>(ent);
+          const unsigned long long wk = t < static_cast<int>(keep) && w >= least ? w : 0;
+          __syncthreads();
+          if (t < static_cast<int>(keep)) S.ent[t] = idx;
+          __syncthreads();
+          int pos = 0;
+          if (t < static_cast<int>(keep))
+            for (int i = 0; i < static_cast<int>(keep); ++i) pos += static_cast<uint32_t>(S.ent[i]) < idx;
+          if (t < static_cast<int>(keep)) S.sorted[pos] = wk;
+          __syncthreads();
+          const unsigned long long v = t < static_cast<int>(keep) ? S.sorted[t] : 0, in = scan(v);
+          if (t == static_cast<int>(keep) - 1) S.left = in;
+          __syncthreads();
+          const unsigned long long sum = S.left, draw = floor_part(u, sum);
+          if (in > draw && in - v <= draw) S.pick = t;
+          __syncthreads();
+          if (t < static_cast<int>(keep) && pos == static_cast<int>(S.pick)) emit(idx, ratio(key_value(static_cast<uint32_t>(ent >> 32)), sum));
+          cmd.what = kDone;
         } else {
           // the kept masses of the row's segments, and the one the draw falls in
-          v.status = kWalk;
-          for (int i = t; i < C * NW; i += THREADS) S.all[i] = C > 1 ? peer_load(&S.seg[i % NW], i / NW) : S.seg[i];
-          __syncthreads();
-#pragma unroll
-          for (int e = 0; e < E; ++e) {
-            const int i = t * E + e;
-            if (i < keep && w[e] >= least) atomicAdd(&S.all[~static_cast<uint32_t>(S.ent[i]) / static_cast<uint32_t>(seg_len)], w[e]);
+          if (keep > 0 && !cmd.ties) {
+            cmd.key = static_cast<uint32_t>(S.sorted[keep - 1] >> 32);
+            cmd.tie_limit = ~static_cast<uint32_t>(S.sorted[keep - 1]);
+          } else {
+            cmd.key = cmd.ties ? hi_key : 0xffffffffu;
+            cmd.tie_limit = 0;
+          }
+          if (!cmd.ties && t < static_cast<int>(keep) && w >= least)
+            atomicAdd(&S.all[~static_cast<uint32_t>(ent) / static_cast<uint32_t>(seg_len)], w);
+          if (cmd.ties && t == 0) {  // the first `keep` of the equal logits, segment by segment
+            uint32_t left = keep;
+            for (int i = 0; i < C * NW; ++i) {
+              const uint32_t here = min(left, S.allties[i]);
+              S.allties[i] = here;
+              left -= here;
+              if (tie_w >= least) S.all[i] += here * tie_w;
+            }
           }
           __syncthreads();
           if (t < 32) {
             constexpr int Q = kMaxCluster * NW / 32;
-            unsigned long long own4[Q], s = 0;
+            unsigned long long part[Q], s = 0;
 #pragma unroll
-            for (int i = 0; i < Q; ++i) s += own4[i] = lane * Q + i < C * NW ? S.all[lane * Q + i] : 0;
-            const unsigned long long in = warp_incl(s);
-            const unsigned long long tot = __shfl_sync(0xffffffffu, in, 31);
+            for (int i = 0; i < Q; ++i) s += part[i] = lane * Q + i < C * NW ? S.all[lane * Q + i] : 0;
+            const unsigned long long in = warp_incl(s), tot = __shfl_sync(0xffffffffu, in, 31);
             const unsigned long long draw = floor_part(u, tot);
             const unsigned who = __ballot_sync(0xffffffffu, in > draw);
             if (lane == (who ? __ffs(who) - 1 : 31)) {
               unsigned long long before = in - s;
               int i = 0;
-              while (i < Q - 1 && before + own4[i] <= draw) before += own4[i++];
+#pragma unroll
+              for (int q = 0; q < Q - 1; ++q)
+                if (i == q && before + part[q] <= draw) before += part[q], ++i;
               S.pick = lane * Q + i;
               S.left = draw - before;
               S.pickw = tot;
             }
           }
           __syncthreads();
-          v.segment = S.pick;
-          v.rem_lo = static_cast<uint32_t>(S.left);
-          v.rem_hi = static_cast<uint32_t>(S.left >> 32);
-          v.total_lo = static_cast<uint32_t>(S.pickw);
-          v.total_hi = static_cast<uint32_t>(S.pickw >> 32);
+          cmd.what = kWalk;
+          cmd.segment = S.pick;
+          cmd.tie_keep = cmd.ties ? S.allties[S.pick] : 0;
+          cmd.rem_lo = static_cast<uint32_t>(S.left);
+          cmd.rem_hi = static_cast<uint32_t>(S.left >> 32);
+          cmd.total_lo = static_cast<uint32_t>(S.pickw);
+          cmd.total_hi = static_cast<uint32_t>(S.pickw >> 32);
+        }
+        if (early) {
+          row_wait(C);
+          return;
         }
       }
-      if (early) {
-        if (C > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-        return;
-      }
+    }
+    // ---- the next command, from the first CTA to all
+    if (rank == 0) {
       __syncthreads();
-      constexpr int words = sizeof(Verdict) / 4;
-      const uint32_t* vw = reinterpret_cast<const uint32_t*>(&v);
-      if (t < C) {
-#pragma unroll
-        for (int i = 0; i < words; ++i) {
-          if (C > 1)
-            peer_store(reinterpret_cast<uint32_t*>(&S.v) + i, t, vw[i]);
-          else
-            reinterpret_cast<uint32_t*>(&S.v)[i] = vw[i];
-        }
-      }
-    } else if (early) {
-      // the first CTA goes on alone once it has read the lists
-      asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-      asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-      return;
+      if (t == 0) S.cmd = cmd;
+      __syncthreads();
+      constexpr int words = sizeof(Command) / 4;
+      if (C > 1)
+        for (int i = t; i < (C - 1) * words; i += THREADS)
+          peer_store(reinterpret_cast<uint32_t*>(&S.cmd) + i % words, 1 + i / words,
+                     reinterpret_cast<const uint32_t*>(&S.cmd)[i % words]);
     }
     row_sync(C);
-    v = S.v;
-    if (v.status == kDrawn) return;
-    if (v.status == kWalk) break;
-    // Another list: top-p's border now that top-k's mass is known, or a neighbouring bin, with
-    // the exact mass up to this list's start (or end) in place of its estimate.
-    if (round >= 64) {
+    cmd = S.cmd;
+    if (cmd.what == kDone) return;
+    if (cmd.what == kSlow) {
       if (rank == 0) slow_row<T, THREADS>(a, row, S.tab, SlowScratch{S.red, S.ent, S.ties});
       return;
     }
-    if (v.status == kTopKDone) {
-      whole = (static_cast<unsigned long long>(v.total_hi) << 32) | v.total_lo;
-      count_left = false;
-      if (scale != 1.f) first_window();
-      continue;
-    }
-    const unsigned long long known = (static_cast<unsigned long long>(v.above_hi) << 32) | v.above_lo;
-    const int lo = static_cast<int>((xa - x0) * scale), hi = static_cast<int>((xb - x0) * scale);
-    const int edge = v.status == kLater ? hi : lo;
-    const float delta = static_cast<float>(known) * (1.f / (1ull << kFixBits)) -
-                        (edge > 0 ? S.cm[edge - 1] : base_mass + shift_mass);
-    shift_mass = scale == 1.f ? shift_mass + delta : delta;
-    if (scale != 1.f && (v.status == kLater ? hi > kBins - 1 : lo < 1)) {  // outside the window
-      if (v.status == kLater)
-        first_least = static_cast<int>(x0) + 1;
-      else
-        first_most = static_cast<int>(x0) - 1;
-      first_window();
-    } else {
-      if (v.status == kLater)
-        (scale == 1.f ? first_least : at_least) = hi;
-      else
-        (scale == 1.f ? first_most : at_most) = lo - 1;
-      __syncthreads();
-      for (int i = t; i < kBins; i += THREADS) S.cm[i] += delta;
-      if (scale != 1.f) base_mass += delta, shift_mass = 0.f;
-      __syncthreads();
-    }
+    if (cmd.what == kWalk) break;
   }
 
-  // ---- the draw lies in one segment: its CTA's warps sum an eighth each, one walks its part
-  if (static_cast<int>(v.segment) / NW != rank) return;
-  const int seg_len = slice / NW, s0 = (v.segment % NW) * seg_len;
-  const int part = (seg_len / NW + 31) / 32 * 32;
+  // ---- the draw lies in one segment: its CTA's warps take a part each, one walks its part
+  if (static_cast<int>(cmd.segment) / NW != rank) return;
+  const int s0 = (cmd.segment % NW) * seg_len, part = (seg_len / NW + 31) / 32 * 32;
   const int i0 = s0 + min(seg_len, warp * part), i1 = s0 + min(seg_len, (warp + 1) * part);
-  auto kept_weight = [&](int i) -> unsigned long long {
-    const float l = i < i1 ? at(i) : -INFINITY;
-    const float pl = place(l);
-    if (pl >= xb || pl >= kLastBin) return 0;
-    if (pl >= xa) {
-      const uint32_t key = order_key(l);
-      if (!(key > v.key || (key == v.key && static_cast<uint32_t>(j0 + i) <= v.tie_limit))) return 0;
+  const float xa = cmd.xa, xb = fminf(cmd.xb, kLastBin);
+  auto logit = [&](int i) { return i < i1 ? to_f32<T>(sl[i]) + 0.f : -INFINITY; };
+  uint32_t tie_limit = cmd.tie_limit;
+  if (cmd.ties) {  // the index of the segment's last kept tie
+    auto tied = [&](int i) {
+      const float l = logit(i), pl = place(l);
+      return pl >= xa && pl < xb;
+    };
+    uint32_t here = 0;
+    for (int i = i0; i < i1; i += 32) here += __popc(__ballot_sync(0xffffffffu, tied(i + lane)));
+    if (t == 0) S.tie_at = 0;
+    if (lane == 0) S.segties[warp] = here;
+    __syncthreads();
+    uint32_t before = 0;
+    for (int w = 0; w < warp; ++w) before += S.segties[w];
+    if (cmd.tie_keep > before && cmd.tie_keep <= before + here) {
+      for (int i = i0; i < i1; i += 32) {
+        const unsigned votes = __ballot_sync(0xffffffffu, tied(i + lane));
+        const uint32_t need = cmd.tie_keep - before;
+        if (need <= static_cast<uint32_t>(__popc(votes))) {
+          if ((votes >> lane & 1u) && static_cast<uint32_t>(__popc(votes & ((2u << lane) - 1))) == need)
+            S.tie_at = j0 + i + lane + 1;
+          break;
+        }
+        before += __popc(votes);
+      }
     }
-    const unsigned long long w = weight_fix<kExact>(l, m, c, S.tab);
+    __syncthreads();
+    tie_limit = S.tie_at;  // one past it; 0: none kept
+  }
+  auto kept_weight = [&](int i) -> unsigned long long {
+    const float l = logit(i), pl = place(l);
+    if (pl >= xb) return 0;
+    if (pl >= xa) {
+      const uint32_t key = order_key(l), idx = j0 + i;
+      if (cmd.ties ? idx >= tie_limit : !(key > cmd.key || (key == cmd.key && idx <= tie_limit))) return 0;
+    }
+    const unsigned long long w = weight(l, pl);
     return w >= least ? w : 0;
   };
   unsigned long long sum = 0;
@@ -1102,17 +1112,15 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
   __syncthreads();
   unsigned long long before = 0;
   for (int w = 0; w < warp; ++w) before += S.red[w];
-  const unsigned long long rem = (static_cast<unsigned long long>(v.rem_hi) << 32) | v.rem_lo;
+  const unsigned long long rem = (static_cast<unsigned long long>(cmd.rem_hi) << 32) | cmd.rem_lo;
   if (!(before <= rem && rem < before + sum)) return;
   for (int i = i0; i < i1; i += 32) {
     const unsigned long long w = kept_weight(i + lane);
     const unsigned long long incl = before + warp_incl(w);
     const unsigned hit = __ballot_sync(0xffffffffu, incl > rem);
     if (hit) {
-      if (lane == __ffs(hit) - 1) {
-        const unsigned long long total = (static_cast<unsigned long long>(v.total_hi) << 32) | v.total_lo;
-        emit(j0 + i + lane, static_cast<float>(static_cast<double>(w) / static_cast<double>(total)));
-      }
+      if (lane == __ffs(hit) - 1)
+        emit(j0 + i + lane, ratio(logit(i + lane), (static_cast<unsigned long long>(cmd.total_hi) << 32) | cmd.total_lo));
       return;
     }
     before = __shfl_sync(0xffffffffu, incl, 31);

@@ -348,8 +348,9 @@ def check_sampling(logits, per, temp, k, p, mp, u):
         j, prob, margin = ref.sample_filtered(host[r], f(temp[b]), 0 if k is None else k[b],
                                               1.0 if p is None else float(f(p[b])),
                                               0.0 if mp is None else float(f(mp[b])), float(f(u[r])))
-        # weights are good to 2e-9 of their own and 2^-45 of the largest: a border further than
-        # 2^-26 of the mass cannot be on the other side
+        # weights are good to 2e-9 of their own and 2^-45 of the largest (below 2^-8 of the largest
+        # in a row longer than its list: to 2^-22 of their own, either sign, thousands to a sum): a
+        # border further than 2^-26 of the mass is not expected on the other side
         if margin < 2.0 ** -26:
             near += 1
             continue
