@@ -359,6 +359,7 @@ constexpr int kList = 256;          // entries the first CTA sorts
 constexpr int kBins = 512;          // bins of one window
 constexpr float kPerOctave = 11.f;  // 46 octaves (weights down to 2^-46) in 506 bins
 constexpr int kTopBins = 88;        // bins (8 octaves) with exact weights; below, ex2's 2^-22 will do
+constexpr int kMassBins = 22;       // bins whose masses are summed while counting; below, counts tell them
 constexpr int kLastBin = 507;       // from here on weights are 0
 constexpr int kMaxCluster = 8;
 
@@ -436,7 +437,7 @@ template <int THREADS>
 struct RowSmem {
   float2 tab[32];
   uint32_t cnt[kBins];                // this CTA's counts in the window's bins
-  unsigned long long mass[kTopBins];  // and masses of the top bins
+  unsigned long long mass[kMassBins];  // and, for top-p alone, masses of the top bins
   uint32_t cc[kBins];                 // first CTA: the row's counts up to and including a bin
   float cm[kBins];                    // and masses (estimated from the counts below the top bins)
   unsigned long long ent[kList];      // listed entries: order_key << 32 | ~index
@@ -499,7 +500,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
   mine = warp_max(mine);
   if (lane == 0) S.red[warp] = __float_as_uint(mine);
   for (int i = t; i < kBins; i += THREADS) S.cnt[i] = 0;
-  if (t < kTopBins) S.mass[t] = 0;
+  if (t < kMassBins) S.mass[t] = 0;
   if (C > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   __syncthreads();
   if (t < C) {
@@ -560,6 +561,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
   auto place = [&](float l) { return l == m ? 0.f : fminf(__fmul_rn(__fsub_rn(m, l), per), 511.5f); };
   // a logit below this has a place past `y` (a little below it: places are rounded)
   auto logit_at = [&](float y) { return m < INFINITY ? m - (y + 0.01f) / per * 1.00001f - fabsf(m) * 1e-6f : m; };
+  // and above this, one before `y`
+  auto logit_from = [&](float y) { return y > 0.f ? m - (y - 0.01f) / per * 0.99999f + fabsf(m) * 1e-6f : m; };
   // the weight of a logit at place pl: far from the largest, by ex2 alone (its argument in two
   // parts too: a slope off by one rounding would tilt the whole tail)
   auto ex2_at = [&](float l, float shift) {
@@ -583,12 +586,13 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
   const bool by_count = k < V, by_mass = p < 1.f, by_mass_only = by_mass && !by_count;
   const bool whole_list = V <= kList;
 
-  // Counts the entries in bins b0 up to b1 of the window, and the masses of the top bins; for
-  // top-p alone also the slice's whole mass.
+  // Counts the entries in bins b0 up to b1 of the window; for top-p alone (`want_mass`) also the
+  // top bins' masses and the slice's whole mass, by ex2 below the top bins.
   auto count_bins = [&](const Command& cmd, bool want_mass) {
     unsigned long long sum = 0;
     float low = 0.f;
     const float x0 = cmd.x0, scale = cmd.scale, cut = logit_at(x0 + cmd.b1 / scale);
+    const float past = logit_from(x0 + cmd.b0 / scale);
     const bool first = scale == 1.f;
     for (int i = t * VEC; i < slice; i += THREADS * VEC) {
       const uint4 v = *reinterpret_cast<const uint4*>(sl + i);
@@ -597,12 +601,12 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
       for (int e = 0; e < VEC; ++e) {
         const float l = logit_of<T>(v, e);
         float wf = want_mass ? fmaxf(ex2_at(l, 0.f), 0.f) : 0.f;  // NaN: nothing
-        if (l >= cut) {
+        if (l >= cut && l <= past) {
           const float pl = place(l), y = first ? pl : (pl - x0) * scale;
           if (y >= cmd.b0 && y < cmd.b1) {
             const int bin = static_cast<int>(y);
             atomicAdd(&S.cnt[bin], 1u);
-            if (first && bin < kTopBins) {
+            if (want_mass && bin < kMassBins) {
               const unsigned long long w = weight_fix<kExact>(l, m, c, S.tab);
               atomicAdd(&S.mass[bin], w);
               sum += w;
@@ -628,6 +632,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
   float base_mass = 0.f, shift = 0.f;  // mass before the window; what an exact sum has shown its estimate to lack
   int first_least = 0, first_most = kBins - 1, at_least = 0, at_most = kBins - 1;  // bounds of the border's bin
   int lim = 0;                         // bins of the first window counted so far
+  bool masses = false;                 // the top bins' masses have been summed
 
   // The row's running counts and masses over the window's bins, into S.cc and S.cm.
   auto total_bins = [&](const Command& cmd) {
@@ -642,7 +647,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
       ms[i] = 0.f;
       if (bin < cmd.b1) {
         cs[i] = row_total(&S.cnt[bin]);
-        if (first && bin < kTopBins)
+        if (masses && bin < kMassBins)
           ms[i] = static_cast<float>(row_total(&S.mass[bin])) * (1.f / (1ull << kFixBits));
         else
           ms[i] = cs[i] * exp2f(-(cmd.x0 + (bin + 0.5f) / cmd.scale) / kPerOctave);
@@ -751,7 +756,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
     if (cmd.what == kCount) {
       if (cmd.fresh) {
         for (int i = t; i < kBins; i += THREADS) S.cnt[i] = 0;
-        if (t < kTopBins) S.mass[t] = 0;
+        if (t < kMassBins) S.mass[t] = 0;
         __syncthreads();
       }
       count_bins(cmd, by_mass_only && round == 0);
@@ -760,6 +765,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
         if (by_mass_only && round == 0) whole = row_total(&S.own[0]);
         Command all = cmd;
         all.b0 = 0;
+        masses = by_mass_only && round == 0;
         total_bins(all);
         cmd = choose(cmd);
       }
