@@ -358,8 +358,10 @@ __device__ __noinline__ void slow_row(const SampleFilteredArgs& a, int row, cons
 constexpr int kList = 256;          // entries the first CTA sorts
 constexpr int kBins = 512;          // bins of one window
 constexpr float kPerOctave = 11.f;  // 46 octaves (weights down to 2^-46) in 506 bins
-constexpr int kTopBins = 88;        // bins (8 octaves) with exact weights; below, ex2's 2^-22 will do
-constexpr int kMassBins = 22;       // bins whose masses are summed while counting; below, counts tell them
+// Bins (6 octaves) whose weights are exact wherever they are summed: what ex2's error of 2^-22
+// does to a sum of smaller ones averages out (64 of them at least for a share worth a weight).
+constexpr int kTopBins = 66;
+constexpr int kFirstBins = 88, kSecondBins = 198;  // a top-k row counts 8 octaves first, then 18, then all
 constexpr int kLastBin = 507;       // from here on weights are 0
 constexpr int kMaxCluster = 8;
 
@@ -437,7 +439,7 @@ template <int THREADS>
 struct RowSmem {
   float2 tab[32];
   uint32_t cnt[kBins];                // this CTA's counts in the window's bins
-  unsigned long long mass[kMassBins];  // and, for top-p alone, masses of the top bins
+  unsigned long long mass[kTopBins];  // and, for top-p alone, masses of the top bins
   uint32_t cc[kBins];                 // first CTA: the row's counts up to and including a bin
   float cm[kBins];                    // and masses (estimated from the counts below the top bins)
   unsigned long long ent[kList];      // listed entries: order_key << 32 | ~index
@@ -453,6 +455,9 @@ struct RowSmem {
   Command cmd;
 };
 
+// A cluster of C CTAs per row, each with `slice` of its entries in shared memory. (A CTA per row
+// that reads it again from L2 was slower: 1024 rows of 152k bf16 logits in flight two per SM
+// do not stay in L2.)
 template <typename T, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kernel(const SampleFilteredArgs a, int C, int slice) {
   constexpr int NW = THREADS / 32, VEC = 16 / sizeof(T);
@@ -477,30 +482,62 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
   float u = __ldcg(a.uniforms + row);
   u = u > 0.f ? fminf(u, 0.99999994f) : 0.f;
 
-  // ---- the slice into shared memory, and its largest logit
-  const int j0 = rank * slice, n = max(0, min(slice, V - j0));
-  const T* src = lr + j0;
+  // This CTA's entries are vectors 0 .. nvec of 16 bytes, entry e of vector i being index
+  // j0 + i VEC + e; warp w's segment is seg_vecs of them.
+  const int j0 = rank * slice, nvec = slice / VEC, seg_vecs = nvec / NW;
+  auto load = [&](int i) { return *reinterpret_cast<const uint4*>(sl + i * VEC); };
+  // f(entry, its logit) for the entries of a vector from `cut` to `past`: the lanes of a warp
+  // take their first ones together, then their second ones
+  auto each_between = [&](const uint4& v, float cut, float past, auto f) {
+    uint32_t hits = 0;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      const float l = logit_of<T>(v, e);
+      if (l >= cut && l <= past) hits |= 1u << e;
+    }
+    while (hits) {
+      const int e = __ffs(hits) - 1, word = e / (VEC / 4);
+      hits &= hits - 1;
+      const uint32_t x = word < 2 ? (word == 0 ? v.x : v.y) : (word == 2 ? v.z : v.w);
+      f(e, (sizeof(T) == 4 ? __uint_as_float(x) : __uint_as_float(e & 1 ? x & 0xffff0000u : x << 16)) + 0.f);
+    }
+  };
+
+  // ---- the slice into shared memory, and the row's largest logit
   float mine = -INFINITY;
-  int done = 0;
-  if ((reinterpret_cast<uintptr_t>(lr) & 15) == 0) {
-    done = n / VEC * VEC;
+  int where = 0;  // the thread's first vector that holds its largest logit
+  auto see = [&](int i, const uint4& v) {
+    const float x = largest<T>(v);
+    if (x > mine) {
+      mine = x;
+      where = i;
+    }
+  };
+  {
+    const int n = max(0, min(slice, V - j0));
+    const T* src = lr + j0;
+    int done = 0;
+    if ((reinterpret_cast<uintptr_t>(lr) & 15) == 0) {
+      done = n / VEC * VEC;
 #pragma unroll 4
-    for (int i = t * VEC; i < done; i += THREADS * VEC) {
-      const uint4 v = __ldcs(reinterpret_cast<const uint4*>(src + i));
-      *reinterpret_cast<uint4*>(sl + i) = v;
-      mine = fmaxf(mine, largest<T>(v));
+      for (int i = t; i < done / VEC; i += THREADS) {
+        const uint4 v = __ldcs(reinterpret_cast<const uint4*>(src + i * VEC));
+        *reinterpret_cast<uint4*>(sl + i * VEC) = v;
+        see(i, v);
+      }
+    }
+#pragma unroll 4
+    for (int i = done + t; i < slice; i += THREADS) sl[i] = i < n ? src[i] : from_f32<T>(-INFINITY);
+    if (done < slice) {
+      __syncthreads();
+      for (int i = done / VEC + t; i < nvec; i += THREADS) see(i, load(i));
     }
   }
-  for (int i = done + t; i < n; i += THREADS) {
-    const T v = src[i];
-    sl[i] = v;
-    mine = fmaxf(mine, to_f32<T>(v));
-  }
-  for (int i = n + t; i < slice; i += THREADS) sl[i] = from_f32<T>(-INFINITY);
+  const float my_top = mine;
   mine = warp_max(mine);
   if (lane == 0) S.red[warp] = __float_as_uint(mine);
   for (int i = t; i < kBins; i += THREADS) S.cnt[i] = 0;
-  if (t < kMassBins) S.mass[t] = 0;
+  if (t < kTopBins) S.mass[t] = 0;
   if (C > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   __syncthreads();
   if (t < C) {
@@ -540,18 +577,19 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
     while (__uint_as_float(S.top[owner]) != m) ++owner;
     if (rank != owner) return;
     int best = INT_MAX;
-    for (int i = t; i < n; i += THREADS)
-      if (to_f32<T>(sl[i]) == m) {
-        best = i;
-        break;
-      }
+    if (my_top == m) {
+      const uint4 v = load(where);
+#pragma unroll
+      for (int e = VEC - 1; e >= 0; --e)
+        if (logit_of<T>(v, e) == m) best = j0 + where * VEC + e;
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) best = min(best, __shfl_xor_sync(0xffffffffu, best, o));
     if (lane == 0) S.ties[warp] = best;
     __syncthreads();
     if (t == 0) {
       for (int w = 1; w < NW; ++w) best = min(best, S.ties[w]);
-      emit(j0 + best, 1.f);
+      emit(best, 1.f);
     }
     return;
   }
@@ -563,22 +601,23 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
   auto logit_at = [&](float y) { return m < INFINITY ? m - (y + 0.01f) / per * 1.00001f - fabsf(m) * 1e-6f : m; };
   // and above this, one before `y`
   auto logit_from = [&](float y) { return y > 0.f ? m - (y - 0.01f) / per * 0.99999f + fabsf(m) * 1e-6f : m; };
-  // the weight of a logit at place pl: far from the largest, by ex2 alone (its argument in two
-  // parts too: a slope off by one rounding would tilt the whole tail)
+  // exp((l - m) / T) 2^shift by ex2, its argument in two parts too: a slope off by a rounding
+  // would tilt the whole tail
   auto ex2_at = [&](float l, float shift) {
     const float d = __fsub_rn(l, m);
     float e;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(__fmaf_rn(d, c.hi, __fmaf_rn(d, c.lo, shift))));
     return e;
   };
-  auto weight = [&](float l, float pl) -> unsigned long long {
-    if (pl < kTopBins) return weight_fix<kExact>(l, m, c, S.tab);
+  // The weight of a logit at place pl. Those that are kept whatever the border (`summed`, many)
+  // are good to 2^-22 below the top bins; a listed one is exact. The same entry has the same
+  // weight in a segment's sum and in its walk.
+  auto weight = [&](float l, float pl, bool summed) -> unsigned long long {
+    if (!summed || pl < kTopBins) return weight_fix<kExact>(l, m, c, S.tab);
     return pl < kLastBin ? __float2ull_rn(ex2_at(l, static_cast<float>(kFixBits))) : 0;
   };
-  auto key_weight = [&](uint32_t key) {
-    const float l = key_value(key);
-    return weight(l, place(l));
-  };
+  auto key_weight = [&](uint32_t key) { return weight_fix<kExact>(key_value(key), m, c, S.tab); };
+  const bool plain = m < INFINITY && per > 0.f && per < INFINITY;  // no 0 times infinity in a place
   auto ratio = [&](float l, unsigned long long sum) {  // the probability of a drawn logit
     return static_cast<float>(static_cast<double>(weight_fix<kExact>(l, m, c, S.tab)) / static_cast<double>(sum));
   };
@@ -586,42 +625,44 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
   const bool by_count = k < V, by_mass = p < 1.f, by_mass_only = by_mass && !by_count;
   const bool whole_list = V <= kList;
 
-  // Counts the entries in bins b0 up to b1 of the window; for top-p alone (`want_mass`) also the
-  // top bins' masses and the slice's whole mass, by ex2 below the top bins.
-  auto count_bins = [&](const Command& cmd, bool want_mass) {
+  // Counts the entries in bins b0 up to b1 of the window.
+  auto count_bins = [&](const Command& cmd) {
+    const float x0 = cmd.x0, scale = cmd.scale;
+    const float cut = logit_at(x0 + cmd.b1 / scale), past = logit_from(x0 + cmd.b0 / scale);
+    for (int i = t; i < nvec; i += THREADS) {
+      const uint4 v = load(i);
+      if (largest<T>(v) < cut) continue;
+      each_between(v, cut, past, [&](int, float l) {
+        const float y = (place(l) - x0) * scale;
+        if (y >= cmd.b0 && y < cmd.b1) atomicAdd(&S.cnt[static_cast<int>(y)], 1u);
+      });
+    }
+  };
+  // For top-p alone: counts all bins, and sums the slice's mass and the top bins' masses.
+  auto count_and_weigh = [&]() {
     unsigned long long sum = 0;
     float low = 0.f;
-    const float x0 = cmd.x0, scale = cmd.scale, cut = logit_at(x0 + cmd.b1 / scale);
-    const float past = logit_from(x0 + cmd.b0 / scale);
-    const bool first = scale == 1.f;
-    for (int i = t * VEC; i < slice; i += THREADS * VEC) {
-      const uint4 v = *reinterpret_cast<const uint4*>(sl + i);
-      if (!want_mass && largest<T>(v) < cut) continue;
+    for (int i = t; i < nvec; i += THREADS) {
+      const uint4 v = load(i);
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
         const float l = logit_of<T>(v, e);
-        float wf = want_mass ? fmaxf(ex2_at(l, 0.f), 0.f) : 0.f;  // NaN: nothing
-        if (l >= cut && l <= past) {
-          const float pl = place(l), y = first ? pl : (pl - x0) * scale;
-          if (y >= cmd.b0 && y < cmd.b1) {
-            const int bin = static_cast<int>(y);
-            atomicAdd(&S.cnt[bin], 1u);
-            if (want_mass && bin < kMassBins) {
-              const unsigned long long w = weight_fix<kExact>(l, m, c, S.tab);
-              atomicAdd(&S.mass[bin], w);
-              sum += w;
-              wf = 0.f;
-            }
+        const float pl = plain ? fminf(__fmul_rn(__fsub_rn(m, l), per), 511.5f) : place(l);
+        if (pl < kLastBin) {
+          atomicAdd(&S.cnt[static_cast<int>(pl)], 1u);
+          if (pl < kTopBins) {
+            const unsigned long long w = weight(l, pl, true);
+            atomicAdd(&S.mass[static_cast<int>(pl)], w);
+            sum += w;
+          } else {
+            low += ex2_at(l, 0.f);
           }
         }
-        low += wf;
       }
     }
-    if (want_mass) {
-      sum += __float2ull_rn(low * static_cast<float>(1ull << kFixBits));
-      sum = block_sum_u64<THREADS>(sum, S.red);
-      if (t == 0) S.own[0] = sum;
-    }
+    sum += __float2ull_rn(low * static_cast<float>(1ull << kFixBits));
+    sum = block_sum_u64<THREADS>(sum, S.red);
+    if (t == 0) S.own[0] = sum;
   };
 
   // ---- the first CTA's knowledge of the borders
@@ -637,7 +678,6 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
   // The row's running counts and masses over the window's bins, into S.cc and S.cm.
   auto total_bins = [&](const Command& cmd) {
     constexpr int PER = kBins / THREADS;
-    const bool first = cmd.scale == 1.f;
     uint32_t cs[PER], csum = 0;
     float ms[PER], msum = 0.f;
 #pragma unroll
@@ -647,7 +687,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
       ms[i] = 0.f;
       if (bin < cmd.b1) {
         cs[i] = row_total(&S.cnt[bin]);
-        if (masses && bin < kMassBins)
+        if (masses && bin < kTopBins)
           ms[i] = static_cast<float>(row_total(&S.mass[bin])) * (1.f / (1ull << kFixBits));
         else
           ms[i] = cs[i] * exp2f(-(cmd.x0 + (bin + 0.5f) / cmd.scale) / kPerOctave);
@@ -698,7 +738,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
     if (B == kBins && first && lim < kLastBin) {  // below the bins counted so far
       cmd.what = kCount;
       cmd.b0 = lim;
-      cmd.b1 = lim = kLastBin;
+      cmd.b1 = lim = lim < kSecondBins ? kSecondBins : kLastBin;
       return cmd;
     }
     if (B == kBins) B = last;  // all that has weight, or a mass estimated too low
@@ -749,17 +789,17 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
     cmd.early = 1;
   } else {
     cmd.what = kCount;
-    cmd.b1 = lim = by_mass_only ? kLastBin : kTopBins;
+    cmd.b1 = lim = by_mass_only ? kLastBin : kFirstBins;
   }
-  const int seg_len = slice / NW;
+  const int seg_len = seg_vecs * VEC;
   for (int round = 0;; ++round) {
     if (cmd.what == kCount) {
       if (cmd.fresh) {
         for (int i = t; i < kBins; i += THREADS) S.cnt[i] = 0;
-        if (t < kMassBins) S.mass[t] = 0;
+        if (t < kTopBins) S.mass[t] = 0;
         __syncthreads();
       }
-      count_bins(cmd, by_mass_only && round == 0);
+      if (by_mass_only && round == 0) count_and_weigh(); else count_bins(cmd);
       row_sync(C);
       if (rank == 0) {
         if (by_mass_only && round == 0) whole = row_total(&S.own[0]);
@@ -776,29 +816,42 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
       unsigned long long kept = 0, all = 0;
       uint32_t tied = 0, kmin = 0xffffffffu, kmax = 0;
       const float xa = cmd.xa, xb = fminf(cmd.xb, kLastBin), cut = logit_at(xb);
-      for (int i = warp * seg_len + lane * VEC; i < (warp + 1) * seg_len; i += 32 * VEC) {
-        const uint4 q = *reinterpret_cast<const uint4*>(sl + i);
-        if (largest<T>(q) < cut) continue;
+      auto list = [&](int j, float l) {  // of the zone
+        const uint32_t key = order_key(l);
+        if (cmd.ties) {
+          ++tied;
+          kmin = min(kmin, key);
+          kmax = max(kmax, key);
+        } else {
+          const uint32_t pos = atomicAdd(&S.n_list, 1u);
+          if (pos < kList) S.ent[pos] = (static_cast<unsigned long long>(key) << 32) | ~static_cast<uint32_t>(j);
+        }
+      };
+      const int v0 = warp * seg_vecs + lane, v1 = (warp + 1) * seg_vecs;
+      if (xa > 0.f) {
+        for (int i = v0; i < v1; i += 32) {
+          const uint4 q = load(i);
+          if (largest<T>(q) < cut) continue;
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          const float l = logit_of<T>(q, e);
-          if (!(l >= cut)) continue;
-          const float pl = place(l);
-          if (pl >= xb) continue;
-          if (pl < xa) {
-            const unsigned long long w = weight(l, pl);
-            all += w;
-            if (w >= least) kept += w;
-          } else if (cmd.ties) {
-            const uint32_t key = order_key(l);
-            ++tied;
-            kmin = min(kmin, key);
-            kmax = max(kmax, key);
-          } else {
-            const uint32_t pos = atomicAdd(&S.n_list, 1u);
-            if (pos < kList)
-              S.ent[pos] = (static_cast<unsigned long long>(order_key(l)) << 32) | ~static_cast<uint32_t>(j0 + i + e);
+          for (int e = 0; e < VEC; ++e) {
+            const float l = logit_of<T>(q, e);
+            const float pl = plain ? fminf(__fmul_rn(__fsub_rn(m, l), per), 511.5f) : place(l);
+            if (pl < xa && pl < kLastBin) {
+              const unsigned long long w = weight(l, pl, true);
+              all += w;
+              if (w >= least) kept += w;
+            } else if (pl < xb) {
+              list(j0 + i * VEC + e, l);
+            }
           }
+        }
+      } else {
+        for (int i = v0; i < v1; i += 32) {
+          const uint4 q = load(i);
+          if (largest<T>(q) < cut) continue;
+          each_between(q, cut, INFINITY, [&](int e, float l) {
+            if (place(l) < xb) list(j0 + i * VEC + e, l);
+          });
         }
       }
 #pragma unroll
@@ -1106,7 +1159,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
       const uint32_t key = order_key(l), idx = j0 + i;
       if (cmd.ties ? idx >= tie_limit : !(key > cmd.key || (key == cmd.key && idx <= tie_limit))) return 0;
     }
-    const unsigned long long w = weight(l, pl);
+    const unsigned long long w = weight(l, pl, pl < xa);
     return w >= least ? w : 0;
   };
   unsigned long long sum = 0;
@@ -1135,19 +1188,20 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
 
 template <typename T>
 cudaError_t launch_sample(const Launch& L, const SampleFilteredArgs& a) {
-  // CTAs per row: slices of at most 40 KB where 8 CTAs allow it (four CTAs then share an SM),
-  // and more CTAs, down to 2048 entries each, while the rows alone do not fill the GPU.
+  // CTAs per row: slices of at most 96 KB where 8 CTAs allow it, so that two CTAs share an SM
+  // and one's passes run while the other's slice loads; and more CTAs, down to 2048 entries
+  // each, while the rows alone do not fill the GPU.
   int C = 1;
-  while (C < kMaxCluster && (static_cast<int64_t>(a.V) * sizeof(T) > 40960LL * C ||
+  while (C < kMaxCluster && (static_cast<int64_t>(a.V) * sizeof(T) > 98304LL * C ||
                              (static_cast<int64_t>(a.rows) * C < 2 * L.num_sms && a.V > 2048 * C)))
     C *= 2;
-  const int unit = 32 * 8 * 16 / static_cast<int>(sizeof(T));  // a vector per lane and warp
+  // a thread for some 32 entries, 256 of them at least
+  const bool wide = a.V > 8192 * C;
+  const int threads = wide ? 512 : 256;
+  const int unit = threads * 16 / static_cast<int>(sizeof(T));  // a vector per thread
   const int slice = ((a.V + C - 1) / C + unit - 1) / unit * unit;
   const size_t smem = static_cast<size_t>(slice) * sizeof(T);
-  // larger slices leave room for two CTAs per SM or one: wider CTAs then
-  const bool wide = smem > 49152;
   auto kernel = wide ? sample_filtered_kernel<T, 512> : sample_filtered_kernel<T, 256>;
-  const int threads = wide ? 512 : 256;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   return launch_kc(L, kernel, dim3(static_cast<unsigned>(a.rows) * C), dim3(threads), smem, C, a, C, slice);

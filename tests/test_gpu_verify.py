@@ -348,8 +348,8 @@ def check_sampling(logits, per, temp, k, p, mp, u):
         j, prob, margin = ref.sample_filtered(host[r], f(temp[b]), 0 if k is None else k[b],
                                               1.0 if p is None else float(f(p[b])),
                                               0.0 if mp is None else float(f(mp[b])), float(f(u[r])))
-        # weights are good to 2e-9 of their own and 2^-45 of the largest (below 2^-8 of the largest
-        # in a row longer than its list: to 2^-22 of their own, either sign, thousands to a sum): a
+        # weights are good to 2e-9 of their own and 2^-45 of the largest (below 2^-6 of the largest,
+        # where not listed: to 2^-22 of their own, either sign, thousands to a sum): a
         # border further than 2^-26 of the mass is not expected on the other side
         if margin < 2.0 ** -26:
             near += 1
@@ -379,6 +379,27 @@ def test_sampling_matches(V, seed, scale, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V,pad", [(300, 1), (8192, 0), (9001, 2), (60000, 5)])
+def test_sampling_many_rows_as_few(V, pad, dtype):
+    """A batch that gives each row a CTA of its own draws what a small one does; rows at odd offsets."""
+    g = torch.Generator(device="cuda").manual_seed(V)
+    bs = len(GRID) + 1
+    buf = 2.5 * torch.randn((3 * bs, V + pad), generator=g, device="cuda")
+    buf[:, :9] += 8.0
+    few = buf.to(torch.float32 if dtype == "f32" else torch.bfloat16)[:, :V]
+    k, p, mp = [x[0] for x in GRID] + [7], [x[1] for x in GRID] + [0.7], [x[2] for x in GRID] + [0.1]
+    temp = [0.5 + 0.1 * i for i in range(len(GRID))] + [0.0]
+    u = torch.rand(3 * bs, generator=g, device="cuda").tolist()
+    check_sampling(few, 3, temp, k, p, mp, u)
+    tokens, probs = run_sampling(few, 3, temp, k, p, mp, u)
+    times = 10  # 330 rows
+    many = buf.to(few.dtype).repeat(times, 1)[:, :V]
+    t2, p2 = run_sampling(many, 3, temp * times, k * times, p * times, mp * times, u * times)
+    np.testing.assert_array_equal(t2.reshape(times, -1), np.tile(tokens, (times, 1)))
+    np.testing.assert_allclose(p2.reshape(times, -1), np.tile(probs, (times, 1)), rtol=2.0 ** -22, atol=0)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("V", [700, 40000])
 def test_sampling_ties_and_odd_values(V, dtype):
     """Rows of equal logits, ties at a border, signed zeros, infinities, NaN, nothing finite."""
@@ -402,6 +423,11 @@ def test_sampling_ties_and_odd_values(V, dtype):
     for k, p, mp in [(0, 1.0, 0.0), (13, 1.0, 0.0), (0, 0.3021, 0.0), (V // 4, 0.7733, 0.0), (0, 1.0, 1.0),
                      (0, 0.9137, 0.3)]:
         check_sampling(logits, 1, [1.0] * 10, [k] * 10, [p] * 10, [mp] * 10, u)
+        # as many rows as fill the GPU with a CTA each
+        few = run_sampling(logits, 1, [1.0] * 10, [k] * 10, [p] * 10, [mp] * 10, u)
+        many = run_sampling(logits.repeat(32, 1), 1, [1.0] * 320, [k] * 320, [p] * 320, [mp] * 320, u * 32)
+        for a, b in zip(few, many):
+            np.testing.assert_array_equal(np.tile(a, 32), b)
     tokens, probs = run_sampling(logits, 1, [0.0] * 10, None, None, None, u)
     assert tokens.tolist() == [0, 0, V // 3, 5, 0, 0, 3, V // 2, int(logits[8].float().argmax()), 11]
     assert probs[4] == probs[5] == 0 and (probs[[0, 1, 2, 3, 6, 7, 8, 9]] == 1).all()
