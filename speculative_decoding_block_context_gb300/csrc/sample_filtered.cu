@@ -364,6 +364,8 @@ constexpr int kTopBins = 66;
 constexpr int kFirstBins = 88, kSecondBins = 198;  // a top-k row counts 8 octaves first, then 18, then all
 constexpr int kLastBin = 507;       // from here on weights are 0
 constexpr int kMaxCluster = 8;
+constexpr int kChunks = 4;          // parts in which a slice is loaded
+constexpr int kQuick = 64;          // top-k up to this lists its candidates without counting
 
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -402,6 +404,26 @@ __device__ __forceinline__ void row_sync(int C) {  // every CTA of the row's clu
   row_wait(C);
 }
 
+// Copies `bytes` (a multiple of 16, as both addresses are) into shared memory, counted on bar.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+// Waits for a bulk copy; the clock is looked at only every 256 tries.
+__device__ __forceinline__ void landed(uint64_t* bar, volatile int* gave_up) {
+  uint64_t t0 = 0;
+  for (uint32_t i = 1; !mbar_try_wait(bar, 0); ++i) {
+    if (i & 255) continue;
+    const uint64_t now = globaltimer_ns();
+    if (t0 == 0) t0 = now;
+    if (*gave_up || now - t0 > kWaitLimitNs) {
+      *gave_up = 1;
+      return;
+    }
+  }
+}
 // The largest of 16 bytes of logits (NaN aside).
 template <typename T>
 __device__ __forceinline__ float largest(const uint4& v) {
@@ -452,6 +474,8 @@ struct RowSmem {
   uint32_t n_list, kmin, kmax, pick, tie_at;
   unsigned long long left, pickw;
   int ties[32], bin;
+  uint64_t landed[kChunks];           // a part of the slice has landed
+  int gave_up;
   Command cmd;
 };
 
@@ -470,6 +494,13 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
   if (C > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   if (t < 32) S.tab[t] = kPowers[t];
+  if (t == 0) {
+    for (int q = 0; q < kChunks; ++q) mbar_init(&S.landed[q], 1);
+    S.gave_up = 0;
+    S.n_list = 0, S.kmin = 0xffffffffu, S.kmax = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
   pdl_wait();
   const int rank = C > 1 ? static_cast<int>(cluster_rank()) : 0;
   const int row = blockIdx.x / C, b = row / a.per, V = a.V;
@@ -513,25 +544,29 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
       where = i;
     }
   };
-  {
-    const int n = max(0, min(slice, V - j0));
-    const T* src = lr + j0;
-    int done = 0;
-    if ((reinterpret_cast<uintptr_t>(lr) & 15) == 0) {
-      done = n / VEC * VEC;
-#pragma unroll 4
-      for (int i = t; i < done / VEC; i += THREADS) {
-        const uint4 v = __ldcs(reinterpret_cast<const uint4*>(src + i * VEC));
-        *reinterpret_cast<uint4*>(sl + i * VEC) = v;
-        see(i, v);
+  const int n = max(0, min(slice, V - j0));
+  if ((reinterpret_cast<uintptr_t>(lr) & 15) == 0) {
+    // bulk copies, all in flight at once; entries past the last whole vector by hand
+    const int whole_vecs = n / VEC, chunk = (nvec / THREADS + kChunks - 1) / kChunks * THREADS;
+    if (t == 0) {
+      for (int q = 0; q < kChunks; ++q) {
+        const int v0 = q * chunk, vecs = min(chunk, whole_vecs - v0);
+        if (vecs <= 0) break;
+        mbar_arrive_expect_tx(&S.landed[q], vecs * 16u);
+        bulk_load(sl + v0 * VEC, lr + j0 + v0 * VEC, vecs * 16u, &S.landed[q]);
       }
     }
-#pragma unroll 4
-    for (int i = done + t; i < slice; i += THREADS) sl[i] = i < n ? src[i] : from_f32<T>(-INFINITY);
-    if (done < slice) {
-      __syncthreads();
-      for (int i = done / VEC + t; i < nvec; i += THREADS) see(i, load(i));
+    for (int i = whole_vecs * VEC + t; i < slice; i += THREADS) sl[i] = i < n ? lr[j0 + i] : from_f32<T>(-INFINITY);
+    __syncthreads();
+    for (int q = 0; q * chunk < nvec; ++q) {
+      if (q * chunk < whole_vecs) landed(&S.landed[q], &S.gave_up);
+      for (int i = q * chunk + t; i < min(nvec, (q + 1) * chunk); i += THREADS) see(i, load(i));
     }
+  } else {
+#pragma unroll 8
+    for (int i = t; i < slice; i += THREADS) sl[i] = i < n ? lr[j0 + i] : from_f32<T>(-INFINITY);
+    __syncthreads();
+    for (int i = t; i < nvec; i += THREADS) see(i, load(i));
   }
   const float my_top = mine;
   mine = warp_max(mine);
@@ -540,13 +575,65 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
   if (t < kTopBins) S.mass[t] = 0;
   if (C > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   __syncthreads();
+  const Slope c = slope_of(temp);
+  const float per = c.hi * kPerOctave;
+  const bool by_count = k < V, by_mass = p < 1.f, by_mass_only = by_mass && !by_count;
+  float slice_top = -INFINITY;
+  for (int w = 0; w < NW; ++w) slice_top = fmaxf(slice_top, __uint_as_float(static_cast<uint32_t>(S.red[w])));
+  // A small top-k needs no counting: where k threads' largest logits lie, at least k logits
+  // do, and few more. Each slice lists its own down to there, before the row's maximum is known.
+  const bool quick = by_count && k <= kQuick && !greedy;
+  if (quick) {
+    if (slice_top < INFINITY && per > 0.f && per < INFINITY) {
+      if (my_top > -INFINITY) {
+        const float pl = fminf(__fmul_rn(__fsub_rn(slice_top, my_top), per), 511.f);
+        atomicAdd(&S.cnt[static_cast<int>(pl)], 1u);
+      }
+      __syncthreads();
+      if (t < 32) {  // the first bin down to which k of them lie
+        uint32_t h[kBins / 32], s = 0;
+#pragma unroll
+        for (int i = 0; i < kBins / 32; ++i) s += h[i] = S.cnt[lane * (kBins / 32) + i];
+        const uint32_t in = warp_incl(s);
+        const unsigned who = __ballot_sync(0xffffffffu, in >= static_cast<uint32_t>(k));
+        if (lane == (who ? __ffs(who) - 1 : 31)) {
+          uint32_t before = in - s;
+          int bin = 0;
+#pragma unroll
+          for (int i = 0; i < kBins / 32 - 1; ++i)
+            if (bin == i && before + h[i] < static_cast<uint32_t>(k)) before += h[i], ++bin;
+          S.bin = lane * (kBins / 32) + bin;
+        }
+      }
+      __syncthreads();
+      const float end = fminf(static_cast<float>(S.bin + 1), kLastBin);
+      const float cut = slice_top - (end + 0.01f) / per * 1.00001f - fabsf(slice_top) * 1e-6f;
+      for (int i = t; i < nvec; i += THREADS) {
+        const uint4 v = load(i);
+        if (!(largest<T>(v) >= cut)) continue;
+        each_between(v, cut, INFINITY, [&](int e, float l) {
+          if (__fmul_rn(__fsub_rn(slice_top, l), per) < end) {
+            const uint32_t pos = atomicAdd(&S.n_list, 1u);
+            if (pos < kList)
+              S.ent[pos] = (static_cast<unsigned long long>(order_key(l)) << 32) | ~static_cast<uint32_t>(j0 + i * VEC + e);
+          }
+        });
+      }
+      for (int i = t; i < kBins; i += THREADS) S.cnt[i] = 0;
+      if (t == 0) S.own[1] = 0;
+    } else if (t == 0) {
+      S.n_list = kList + 1;  // infinite logits or slopes: counted below
+    }
+    __syncthreads();
+  }
   if (t < C) {
-    float x = -INFINITY;
-    for (int w = 0; w < NW; ++w) x = fmaxf(x, __uint_as_float(static_cast<uint32_t>(S.red[w])));
-    if (C > 1)
-      peer_store(&S.top[rank], t, __float_as_uint(x));
-    else
-      S.top[0] = __float_as_uint(x);
+    if (C > 1) {
+      peer_store(&S.top[rank], t, __float_as_uint(slice_top));
+      peer_store(&S.found[rank], t, S.n_list);
+    } else {
+      S.top[0] = __float_as_uint(slice_top);
+      S.found[0] = S.n_list;
+    }
   }
   row_sync(C);
   float m = -INFINITY;
@@ -593,8 +680,6 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
     }
     return;
   }
-  const Slope c = slope_of(temp);
-  const float per = c.hi * kPerOctave;
   // place of a logit in units of bins, 0 at the largest; NaN and what has no weight at the end
   auto place = [&](float l) { return l == m ? 0.f : fminf(__fmul_rn(__fsub_rn(m, l), per), 511.5f); };
   // a logit below this has a place past `y` (a little below it: places are rounded)
@@ -622,7 +707,6 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
     return static_cast<float>(static_cast<double>(weight_fix<kExact>(l, m, c, S.tab)) / static_cast<double>(sum));
   };
   const unsigned long long least = least_weight(mp);
-  const bool by_count = k < V, by_mass = p < 1.f, by_mass_only = by_mass && !by_count;
   const bool whole_list = V <= kList;
 
   // Counts the entries in bins b0 up to b1 of the window.
@@ -642,22 +726,28 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
   auto count_and_weigh = [&]() {
     unsigned long long sum = 0;
     float low = 0.f;
+    auto one = [&](float l, float pl) {
+      if (pl < kLastBin) {  // not a NaN
+        atomicAdd(&S.cnt[static_cast<int>(pl)], 1u);
+        if (pl < kTopBins) {
+          const unsigned long long w = weight(l, pl, true);
+          atomicAdd(&S.mass[static_cast<int>(pl)], w);
+          sum += w;
+        } else {
+          low += ex2_at(l, 0.f);
+        }
+      }
+    };
     for (int i = t; i < nvec; i += THREADS) {
       const uint4 v = load(i);
+      if (plain) {
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const float l = logit_of<T>(v, e);
-        const float pl = plain ? fminf(__fmul_rn(__fsub_rn(m, l), per), 511.5f) : place(l);
-        if (pl < kLastBin) {
-          atomicAdd(&S.cnt[static_cast<int>(pl)], 1u);
-          if (pl < kTopBins) {
-            const unsigned long long w = weight(l, pl, true);
-            atomicAdd(&S.mass[static_cast<int>(pl)], w);
-            sum += w;
-          } else {
-            low += ex2_at(l, 0.f);
-          }
+        for (int e = 0; e < VEC; ++e) {
+          const float l = logit_of<T>(v, e);
+          one(l, __fmul_rn(__fsub_rn(m, l), per));
         }
+      } else {
+        each_between(v, -INFINITY, INFINITY, [&](int, float l) { one(l, place(l)); });
       }
     }
     sum += __float2ull_rn(low * static_cast<float>(1ull << kFixBits));
@@ -778,12 +868,15 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
     return cmd;
   };
 
+  uint32_t listed = 0;
+  for (int r = 0; r < C; ++r) listed += S.found[r];
+  const bool all_listed = quick && listed <= kList;
   Command cmd{};
   cmd.scale = 1.f;
   if (!by_count && !by_mass) {
     cmd.what = kPass;
     cmd.xa = cmd.xb = INFINITY;
-  } else if (whole_list) {
+  } else if (whole_list || all_listed) {
     cmd.what = kPass;
     cmd.xb = kLastBin;
     cmd.early = 1;
@@ -810,7 +903,9 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
         cmd = choose(cmd);
       }
     } else {
+     if (!all_listed) {
       // ---- one pass: sum what is kept anyhow (per warp's segment), list the rest
+      __syncthreads();
       if (t == 0) S.n_list = 0, S.kmin = 0xffffffffu, S.kmax = 0;
       __syncthreads();
       unsigned long long kept = 0, all = 0;
@@ -828,14 +923,36 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
         }
       };
       const int v0 = warp * seg_vecs + lane, v1 = (warp + 1) * seg_vecs;
-      if (xa > 0.f) {
+      if (xa > 0.f && plain && least == 0) {
+        // Small weights are added up in float32 per thread: a segment's sum is then off by some
+        // 2^-24 of it, which moves a draw by less than the weights' own error.
+        const float xa1 = fminf(xa, kLastBin);
+        float low = 0.f;
         for (int i = v0; i < v1; i += 32) {
           const uint4 q = load(i);
           if (largest<T>(q) < cut) continue;
 #pragma unroll
           for (int e = 0; e < VEC; ++e) {
             const float l = logit_of<T>(q, e);
-            const float pl = plain ? fminf(__fmul_rn(__fsub_rn(m, l), per), 511.5f) : place(l);
+            const float pl = __fmul_rn(__fsub_rn(m, l), per);
+            if (pl < xa1) {
+              if (pl < kTopBins)
+                kept += weight(l, pl, true);
+              else
+                low += ex2_at(l, 0.f);
+            } else if (pl < xb) {
+              list(j0 + i * VEC + e, l);
+            }
+          }
+        }
+        kept += __float2ull_rn(low * static_cast<float>(1ull << kFixBits));
+        all = kept;
+      } else if (xa > 0.f) {
+        for (int i = v0; i < v1; i += 32) {
+          const uint4 q = load(i);
+          if (largest<T>(q) < cut) continue;
+          each_between(q, cut, INFINITY, [&](int e, float l) {
+            const float pl = place(l);
             if (pl < xa && pl < kLastBin) {
               const unsigned long long w = weight(l, pl, true);
               all += w;
@@ -843,7 +960,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
             } else if (pl < xb) {
               list(j0 + i * VEC + e, l);
             }
-          }
+          });
         }
       } else {
         for (int i = v0; i < v1; i += 32) {
@@ -885,6 +1002,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
         }
       }
       row_sync(C);
+     }
       const bool early = cmd.early;
       if (early && rank != 0) {  // the first CTA goes on alone once it has read the lists
         row_arrive(C);
@@ -1171,7 +1289,12 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
   __syncthreads();
   unsigned long long before = 0;
   for (int w = 0; w < warp; ++w) before += S.red[w];
-  const unsigned long long rem = (static_cast<unsigned long long>(cmd.rem_hi) << 32) | cmd.rem_lo;
+  const unsigned long long rem0 = (static_cast<unsigned long long>(cmd.rem_hi) << 32) | cmd.rem_lo;
+  // (a segment summed in float32 may come out a little smaller here: then its last entry is drawn)
+  unsigned long long segment = before + sum;
+  for (int w = warp + 1; w < NW; ++w) segment += S.red[w];
+  const unsigned long long rem = min(rem0, segment - 1);
+  if (segment == 0 && t == 0) emit(j0 + s0, 0.f);
   if (!(before <= rem && rem < before + sum)) return;
   for (int i = i0; i < i1; i += 32) {
     const unsigned long long w = kept_weight(i + lane);
