@@ -11,11 +11,11 @@
 // 64 bits in whatever order.
 //
 // A row is held in the shared memory of a cluster of CTAs, so that it is read from memory
-// once. Its entries are counted in bins of x = (m - l) * 11 log2(e) / T, eleven bins per
+// once. Its entries are counted in bins of x = (m - l) * 22 log2(e) / T, 22 bins per
 // factor of two in weight; counts and masses of the bins say in which bin a border must lie.
 // Entries of lower x are kept wherever in that bin the border is, so only their weights are
 // summed, per warp's segment of the row; the bin's own entries (a finer bin's where they are
-// more than kList) go to the first CTA, which sorts them, finds the exact border and the
+// more than it has threads) go to the first CTA, which sorts them, finds the exact border and the
 // segment in which the draw falls (or the draw itself where the list starts at the top). That
 // segment's CTA walks it. Equal logits need no list: the border is a number of them.
 //
@@ -355,14 +355,12 @@ __device__ __noinline__ void slow_row(const SampleFilteredArgs& a, int row, cons
 
 // ------------------------------------------------------------------ the cluster's row
 
-constexpr int kList = 256;          // entries the first CTA sorts
-constexpr int kBins = 512;          // bins of one window
-constexpr float kPerOctave = 11.f;  // 46 octaves (weights down to 2^-46) in 506 bins
+constexpr int kBins = 1024;         // bins of one window
+constexpr float kPerOctave = 22.f;  // 46 octaves (weights down to 2^-46) in 1012 bins
 // Bins (6 octaves) whose weights are exact wherever they are summed: what ex2's error of 2^-22
 // does to a sum of smaller ones averages out (64 of them at least for a share worth a weight).
-constexpr int kTopBins = 66;
-constexpr int kFirstBins = 88, kSecondBins = 198;  // a top-k row counts 8 octaves first, then 18, then all
-constexpr int kLastBin = 507;       // from here on weights are 0
+constexpr int kTopBins = 132;
+constexpr int kLastBin = 1014;       // from here on weights are 0
 constexpr int kMaxCluster = 8;
 constexpr int kChunks = 4;          // parts in which a slice is loaded
 constexpr int kQuick = 64;          // top-k up to this lists its candidates without counting
@@ -464,8 +462,8 @@ struct RowSmem {
   unsigned long long mass[kTopBins];  // and, for top-p alone, masses of the top bins
   uint32_t cc[kBins];                 // first CTA: the row's counts up to and including a bin
   float cm[kBins];                    // and masses (estimated from the counts below the top bins)
-  unsigned long long ent[kList];      // listed entries: order_key << 32 | ~index
-  unsigned long long sorted[kList];
+  unsigned long long ent[THREADS];    // listed entries: order_key << 32 | ~index
+  unsigned long long sorted[THREADS];
   unsigned long long red[32], seg[THREADS / 32], all[kMaxCluster * (THREADS / 32)];
   unsigned long long own[2];          // this CTA's mass; its mass of x < xa
   uint32_t segties[THREADS / 32], allties[kMaxCluster * (THREADS / 32)];
@@ -485,6 +483,7 @@ struct RowSmem {
 template <typename T, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kernel(const SampleFilteredArgs a, int C, int slice) {
   constexpr int NW = THREADS / 32, VEC = 16 / sizeof(T);
+  constexpr int kList = THREADS;  // entries the first CTA sorts, one per thread
   constexpr bool kExact = sizeof(T) == 2;
   extern __shared__ __align__(16) uint8_t row_raw[];
   T* sl = reinterpret_cast<T*>(row_raw);
@@ -586,7 +585,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
   if (quick) {
     if (slice_top < INFINITY && per > 0.f && per < INFINITY) {
       if (my_top > -INFINITY) {
-        const float pl = fminf(__fmul_rn(__fsub_rn(slice_top, my_top), per), 511.f);
+        const float pl = fminf(__fmul_rn(__fsub_rn(slice_top, my_top), per), 1023.f);
         atomicAdd(&S.cnt[static_cast<int>(pl)], 1u);
       }
       __syncthreads();
@@ -681,7 +680,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
     return;
   }
   // place of a logit in units of bins, 0 at the largest; NaN and what has no weight at the end
-  auto place = [&](float l) { return l == m ? 0.f : fminf(__fmul_rn(__fsub_rn(m, l), per), 511.5f); };
+  auto place = [&](float l) { return l == m ? 0.f : fminf(__fmul_rn(__fsub_rn(m, l), per), 1023.5f); };
   // a logit below this has a place past `y` (a little below it: places are rounded)
   auto logit_at = [&](float y) { return m < INFINITY ? m - (y + 0.01f) / per * 1.00001f - fabsf(m) * 1e-6f : m; };
   // and above this, one before `y`
@@ -722,19 +721,23 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
       });
     }
   };
-  // For top-p alone: counts all bins, and sums the slice's mass and the top bins' masses.
-  auto count_and_weigh = [&]() {
+  // Counts all bins of the first window; for top-p alone (kWeigh) also sums the slice's mass and
+  // the top bins' masses.
+  auto count_all = [&](auto weigh) {
+    constexpr bool kWeigh = decltype(weigh)::value;
     unsigned long long sum = 0;
     float low = 0.f;
     auto one = [&](float l, float pl) {
       if (pl < kLastBin) {  // not a NaN
         atomicAdd(&S.cnt[static_cast<int>(pl)], 1u);
-        if (pl < kTopBins) {
-          const unsigned long long w = weight(l, pl, true);
-          atomicAdd(&S.mass[static_cast<int>(pl)], w);
-          sum += w;
-        } else {
-          low += ex2_at(l, 0.f);
+        if constexpr (kWeigh) {
+          if (pl < kTopBins) {
+            const unsigned long long w = weight(l, pl, true);
+            atomicAdd(&S.mass[static_cast<int>(pl)], w);
+            sum += w;
+          } else {
+            low += ex2_at(l, 0.f);
+          }
         }
       }
     };
@@ -750,9 +753,11 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
         each_between(v, -INFINITY, INFINITY, [&](int, float l) { one(l, place(l)); });
       }
     }
-    sum += __float2ull_rn(low * static_cast<float>(1ull << kFixBits));
-    sum = block_sum_u64<THREADS>(sum, S.red);
-    if (t == 0) S.own[0] = sum;
+    if constexpr (kWeigh) {
+      sum += __float2ull_rn(low * static_cast<float>(1ull << kFixBits));
+      sum = block_sum_u64<THREADS>(sum, S.red);
+      if (t == 0) S.own[0] = sum;
+    }
   };
 
   // ---- the first CTA's knowledge of the borders
@@ -762,7 +767,6 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
   uint32_t base_count = 0;             // entries before the window
   float base_mass = 0.f, shift = 0.f;  // mass before the window; what an exact sum has shown its estimate to lack
   int first_least = 0, first_most = kBins - 1, at_least = 0, at_most = kBins - 1;  // bounds of the border's bin
-  int lim = 0;                         // bins of the first window counted so far
   bool masses = false;                 // the top bins' masses have been summed
 
   // The row's running counts and masses over the window's bins, into S.cc and S.cm.
@@ -808,11 +812,11 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
     }
     __syncthreads();
   };
-  // The next command from the window's counts: a list around the border, more counting, or
+  // The next command from the window's counts: a list around the border, or
   // (too many entries in one bin) a window on the bin.
   auto choose = [&](Command cmd) {
     const bool first = cmd.scale == 1.f;
-    const int last = first ? lim - 1 : kBins - 1;
+    const int last = first ? kLastBin - 1 : kBins - 1;
     const float goal = p * (static_cast<float>(whole) * (1.f / (1ull << kFixBits)));
     if (t == 0) S.bin = kBins;
     __syncthreads();
@@ -825,12 +829,6 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
     int B = S.bin;
     __syncthreads();
     cmd.early = cmd.ties = cmd.fresh = 0;
-    if (B == kBins && first && lim < kLastBin) {  // below the bins counted so far
-      cmd.what = kCount;
-      cmd.b0 = lim;
-      cmd.b1 = lim = lim < kSecondBins ? kSecondBins : kLastBin;
-      return cmd;
-    }
     if (B == kBins) B = last;  // all that has weight, or a mass estimated too low
     B = first ? max(first_least, min(B, first_most)) : max(at_least, min(B, at_most));
     cmd.what = kPass;
@@ -845,7 +843,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
     } else if (here <= kList || !first) {
       int lo = B, hi = B;
       if (here > kList) {
-        cmd.ties = 1;  // within 2^(1/5632) of one another: equal logits
+        cmd.ties = 1;  // within 2^(1/22528) of one another: equal logits
       } else if (!count_left) {  // the masses are estimates: take the neighbours too where they fit
         if (lo > 0 && S.cc[hi] - (lo > 1 ? S.cc[lo - 2] : base_count) <= kList) --lo;
         if (hi < last && S.cc[hi + 1] - (lo > 0 ? S.cc[lo - 1] : base_count) <= kList) ++hi;
@@ -875,14 +873,15 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
   cmd.scale = 1.f;
   if (!by_count && !by_mass) {
     cmd.what = kPass;
-    cmd.xa = cmd.xb = INFINITY;
+    // nothing past min-p's own border is kept
+    cmd.xa = cmd.xb = mp > 0.f ? 2.f - log2f(fminf(mp, 1.f)) * kPerOctave : INFINITY;
   } else if (whole_list || all_listed) {
     cmd.what = kPass;
     cmd.xb = kLastBin;
     cmd.early = 1;
   } else {
     cmd.what = kCount;
-    cmd.b1 = lim = by_mass_only ? kLastBin : kFirstBins;
+    cmd.b1 = kLastBin;
   }
   const int seg_len = seg_vecs * VEC;
   for (int round = 0;; ++round) {
@@ -892,7 +891,12 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
         if (t < kTopBins) S.mass[t] = 0;
         __syncthreads();
       }
-      if (by_mass_only && round == 0) count_and_weigh(); else count_bins(cmd);
+      if (cmd.scale != 1.f)
+        count_bins(cmd);
+      else if (by_mass_only && round == 0)
+        count_all(std::true_type());
+      else
+        count_all(std::false_type());
       row_sync(C);
       if (rank == 0) {
         if (by_mass_only && round == 0) whole = row_total(&S.own[0]);
@@ -1110,7 +1114,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
           if (cmd.scale == 1.f) {
             cmd = choose(cmd);
           } else {  // back to the first window
-            cmd.what = kCount, cmd.fresh = 1, cmd.x0 = 0.f, cmd.scale = 1.f, cmd.b0 = 0, cmd.b1 = lim = kLastBin;
+            cmd.what = kCount, cmd.fresh = 1, cmd.x0 = 0.f, cmd.scale = 1.f, cmd.b0 = 0, cmd.b1 = kLastBin;
             base_count = 0, base_mass = 0.f;
           }
         } else if (again) {
@@ -1127,7 +1131,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
             else
               first_most = static_cast<int>(cmd.x0) - 1;
             shift = delta;
-            cmd.what = kCount, cmd.fresh = 1, cmd.x0 = 0.f, cmd.scale = 1.f, cmd.b0 = 0, cmd.b1 = lim = kLastBin;
+            cmd.what = kCount, cmd.fresh = 1, cmd.x0 = 0.f, cmd.scale = 1.f, cmd.b0 = 0, cmd.b1 = kLastBin;
             base_count = 0, base_mass = 0.f;
           } else {
             if (again > 0)
