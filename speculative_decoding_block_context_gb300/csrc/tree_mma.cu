@@ -97,6 +97,24 @@ __device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32
       "r"(a_tmem), "r"(blo), "r"(bhi), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+// TMA of a box, and the bytes a barrier expects, by one lane of a warp in step (for the same
+// reason: eight lanes that each issued one took 80 cycles a box).
+__device__ __forceinline__ void tma_elect(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y,
+                                          uint64_t policy) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+      "@q cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%3, %4}], [%2], %5;\n\t}" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "l"(policy)
+      : "memory");
+}
+__device__ __forceinline__ void expect_elect(uint32_t bar, uint32_t bytes) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+      "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar),
+      "r"(bytes)
+      : "memory");
+}
 __device__ __forceinline__ void commit_elect(uint64_t* bar) {
   asm volatile(
       "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
@@ -236,9 +254,8 @@ __global__ void __launch_bounds__(MmaCfg<HD, MT>::THREADS, 1)
     uint8_t* tiles = ring + (warp == 0 ? 0 : KS * C::TILE);
     const int total_rows = static_cast<int>(a.num_pages) * a.nkv * a.P;  // a box from here on reads zeros
     const uint64_t pol = a.width * a.group <= TM ? l2_policy_evict_first() : l2_policy_evict_last();
-    // lane h * boxes + j requests channels 64 h .. 64 h + 63 of the tile's j-th box
-    const int boxes = TN / box_rows, box = lane % boxes, half = lane / boxes;
-    const uint32_t at = half * HALF + box * box_rows * 128;
+    const int boxes = TN / box_rows;
+    const uint32_t tiles0 = smem_u32(tiles), full0 = smem_u32(full);
     int slot = 0, seq = 0;
     uint32_t phase = 0;
     bool ok = true;
@@ -272,15 +289,24 @@ __global__ void __launch_bounds__(MmaCfg<HD, MT>::THREADS, 1)
           rows32 = row_of((t - w.t0) >> 3, page);
           page = page_of(((t - w.t0) >> 3) + 1);
         }
-        const int row = __shfl_sync(0xffffffffu, rows32, first + box * (box_rows >> 4));
+        int box_row[4];  // the boxes' first rows
+#pragma unroll
+        for (int j = 0; j < 4; ++j) box_row[j] = __shfl_sync(0xffffffffu, rows32, first + (j * (box_rows >> 4) & 3));
         if (warp == 0) {
           const unsigned bits = __ballot_sync(0xffffffffu, rows32 != total_rows) >> first & 0xfu;
           if (lane == 0) blocks_ok[seq % kRing] = static_cast<uint8_t>(bits);
         }
         if (!(ok = warp_wait(&empty[slot], phase ^ 1u, ab))) break;
-        if (lane == 0) mbar_arrive_expect_tx(&full[slot], C::TILE);
-        __syncwarp();
-        if (half < HD / 64) tma_load_2d(tiles + slot * C::TILE + at, map, &full[slot], half * 64, row, pol);
+        const uint32_t bar = full0 + slot * 8, dst = tiles0 + slot * C::TILE;
+        expect_elect(bar, C::TILE);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (j < boxes) {
+#pragma unroll
+            for (int h = 0; h < HD / 64; ++h)
+              tma_elect(dst + h * HALF + j * box_rows * 128, map, bar, h * 64, box_row[j], pol);
+          }
+        }
         ++seq;
         if (++slot == slots) slot = 0, phase ^= 1u;
       }
@@ -390,27 +416,47 @@ __global__ void __launch_bounds__(MmaCfg<HD, MT>::THREADS, 1)
     int n = 0, seq = 0, tree_b = -1;  // the lane's tiles so far, the CTA's
     int joins = 0, others = 0;        // lane 0: joins made, lane 1's tiles in them and in other items
     bool ok = true;
-    while (ok && w.next(a)) {
-      const int item_rows = rows_of(), seq0 = seq;
-      const bool own = own_rows(item_rows);
-      const int rows = own ? min(128, item_rows - m * 128) : item_rows;
-      const bool live = row < rows, warp_live = quad * 32 < rows;
-      const int rr = w.tile_m * TM + (own ? m * 128 : 0) + row, node = rr / a.group;
-      const int64_t q_row = static_cast<int64_t>(w.b) * a.width + node;
-      const int q_head = w.head * a.group + (rr - node * a.group);
-      seq += w.t1 - w.t0;
-      if (own || m == 0) {
-        if (live) {
-          const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
-                                                            q_row * a.q_stride + static_cast<int64_t>(q_head) * HD);
-          uint8_t* dst = sq + (own ? m : 0) * C::QTILE + row * 128;
-          uint4 v[HD / 8];
+    // The rows of an item for this lane, and the one this thread has.
+    struct Rows {
+      bool own, loads, live;  // rows per lane; this lane loads some; this thread has one
+      int rows, node, head;
+      int64_t q_row;
+    };
+    auto rows_for = [&](const Walk<TM, TN>& x) {
+      const int item_rows = min(TM, x.r.n * a.group - x.tile_m * TM);
+      Rows q;
+      q.own = own_rows(item_rows);
+      q.loads = q.own || m == 0;
+      q.rows = q.own ? min(128, item_rows - m * 128) : item_rows;
+      q.live = row < q.rows;
+      const int rr = x.tile_m * TM + (q.own ? m * 128 : 0) + row;
+      q.node = rr / a.group;
+      q.head = x.head * a.group + (rr - q.node * a.group);
+      q.q_row = static_cast<int64_t>(x.b) * a.width + q.node;
+      return q;
+    };
+    // An item's queries: asked for early, and put into shared memory once the products that
+    // read the item before's are done. Then its tree, if it reaches that.
+    struct Query {
+      uint4 v[HD / 8];
+    };
+    auto ask = [&](const Rows& q, Query& qv) {
 #pragma unroll
-          for (int x = 0; x < HD / 8; ++x) v[x] = __ldcg(src + x);
+      for (int x = 0; x < HD / 8; ++x) qv.v[x] = make_uint4(0, 0, 0, 0);
+      if (!q.loads || !q.live) return;
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + q.q_row * a.q_stride +
+                                                        static_cast<int64_t>(q.head) * HD);
 #pragma unroll
-          for (int x = 0; x < HD / 8; ++x) {
-            v[x].x ^= flip, v[x].y ^= flip, v[x].z ^= flip, v[x].w ^= flip;
-            *reinterpret_cast<uint4*>(dst + (x >> 3) * QHALF + (((x & 7) ^ (row & 7)) * 16)) = v[x];
+      for (int x = 0; x < HD / 8; ++x) qv.v[x] = __ldcg(src + x);
+    };
+    auto prepare = [&](const Walk<TM, TN>& x, const Rows& q, Query& qv) {
+      if (q.loads) {
+        if (q.live) {
+          uint8_t* dst = sq + (q.own ? m : 0) * C::QTILE + row * 128;
+#pragma unroll
+          for (int y = 0; y < HD / 8; ++y) {
+            qv.v[y].x ^= flip, qv.v[y].y ^= flip, qv.v[y].z ^= flip, qv.v[y].w ^= flip;
+            *reinterpret_cast<uint4*>(dst + (y >> 3) * QHALF + (((y & 7) ^ (row & 7)) * 16)) = qv.v[y];
           }
         }
         fence_async_smem();
@@ -419,17 +465,30 @@ __global__ void __launch_bounds__(MmaCfg<HD, MT>::THREADS, 1)
       if (lane == 0) {
         if (m == 0) {
           mbar_arrive(&q_ready[0]);
-          if (!own && w.t1 - w.t0 > 1) mbar_arrive(&q_ready[1]);
-        } else if (own) {
+          if (!q.own && x.t1 - x.t0 > 1) mbar_arrive(&q_ready[1]);
+        } else if (q.own) {
           mbar_arrive(&q1_ready);
         }
       }
-      if (a.tree_ids && w.t1 * TN > w.r.ctx && tree_b != w.b) {  // the item reaches the tree
+      if (a.tree_ids && x.t1 * TN > x.r.ctx && tree_b != x.b) {  // the item reaches the tree
         __syncwarp();
-        for (int i = lane; i < w.r.n; i += 32) parent[i] = static_cast<short>(i ? parent_of(a, w.b, i, err) : -1);
+        for (int i = lane; i < x.r.n; i += 32) parent[i] = static_cast<short>(i ? parent_of(a, x.b, i, err) : -1);
         __syncwarp();
-        tree_b = w.b;
+        tree_b = x.b;
       }
+    };
+    bool more = w.next(a);
+    Rows q{};
+    if (more) {
+      Query qv;
+      q = rows_for(w);
+      ask(q, qv);
+      prepare(w, q, qv);
+    }
+    while (ok && more) {
+      const bool own = q.own, live = q.live, warp_live = quad * 32 < q.rows;
+      const int node = q.node, seq0 = seq;
+      seq += w.t1 - w.t0;
       const int first = w.t0 + (own ? 0 : m), step = own ? 1 : 2;
       float mx = -INFINITY, l = 0.f;  // the maximum the weights are taken against, and their sum
       for (int t = first; t < w.t1; t += step) {
@@ -513,29 +572,42 @@ __global__ void __launch_bounds__(MmaCfg<HD, MT>::THREADS, 1)
       }
       if (!ok) break;
       const int tiles1 = own ? w.t1 - w.t0 : (w.t1 - w.t0) / 2;  // lane 1's tiles of the item
+      // The next item's queries go in before this one's output comes out: its first scores run
+      // meanwhile.
+      Walk<TM, TN> w2 = w;
+      more = w2.next(a);
+      Rows q2{};
+      Query qv;
+      if (more) q2 = rows_for(w2);
+      ask(q2, qv);
       if (!own && m == 1) {
         if (tiles1 > 0) {  // lane 0 joins the two outputs
           lane1_ml[row] = make_float2(mx, l);
           __syncwarp();
           if (lane == 0) mbar_arrive(&ml_ready);
         }
+        if (more) prepare(w2, q2, qv);
+        w = w2;
+        q = q2;
         continue;
       }
-      if (!(ok = warp_wait(&pv_done[m][(n - 1) & 1], ((n - 1) >> 1) & 1, ab))) break;
       float f0 = 1.f, f1 = 0.f;
       others += tiles1;
       const bool join = !own && tiles1 > 0;
-      if (join) {
+      if (join) {  // (lane 1 has then seen all its scores)
         if (!(ok = warp_wait(&ml_ready, joins & 1, ab))) break;
         ++joins;
-        if (!(ok = warp_wait(&pv_done[1][(others - 1) & 1], ((others - 1) >> 1) & 1, ab))) break;
         const float2 ml = lane1_ml[row];
         const float to = fmaxf(mx, ml.x);
         f0 = mx == -INFINITY ? 0.f : ex2(mx - to);
         f1 = ml.x == -INFINITY ? 0.f : ex2(ml.x - to);
         l = l * f0 + ml.y * f1;
         mx = to;
+        __syncwarp();
       }
+      if (more) prepare(w2, q2, qv);
+      if (!(ok = warp_wait(&pv_done[m][(n - 1) & 1], ((n - 1) >> 1) & 1, ab))) break;
+      if (join && !(ok = warp_wait(&pv_done[1][(others - 1) & 1], ((others - 1) >> 1) & 1, ab))) break;
       tc_fence_after();
       if (warp_live) {
         if (w.whole) {
@@ -544,7 +616,7 @@ __global__ void __launch_bounds__(MmaCfg<HD, MT>::THREADS, 1)
           f1 *= inv;
         }
         const int64_t part = static_cast<int64_t>(2 * static_cast<int>(blockIdx.x) + (w.first_item ? 0 : 1)) * TM + (own ? m * 128 : 0) + row;
-        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + (q_row * a.nq + q_head) * HD;
+        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + (q.q_row * a.nq + q.head) * HD;
 #pragma unroll
         for (int x = 0; x < HD; x += 32) {
           uint32_t o[32];
@@ -585,6 +657,8 @@ __global__ void __launch_bounds__(MmaCfg<HD, MT>::THREADS, 1)
         mbar_arrive(&o_free[m]);
         if (join) mbar_arrive(&o_free[1]);
       }
+      w = w2;
+      q = q2;
     }
   }
   if (err) set_dev_error(a.dev_err, err);
