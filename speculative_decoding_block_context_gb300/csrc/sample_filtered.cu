@@ -149,6 +149,61 @@ __device__ __forceinline__ unsigned long long block_sum_u64(unsigned long long v
   return t;
 }
 
+// Sorts the values of the first N threads, largest first (all distinct; the others' are 0).
+// Up to 256 each counts the larger ones (100 of them: 3k cycles beside another CTA's passes,
+// exchanges 7k). More are exchanged with partners ever closer, through shared memory (x and
+// y in turn) from warp to warp (512: 10k cycles, counting 14k).
+template <int THREADS>
+__device__ __forceinline__ unsigned long long sort_down(unsigned long long v, int N, unsigned long long* x,
+                                                        unsigned long long* y) {
+  const int t = threadIdx.x;
+  if (N <= 256) {
+    if (t < ((N + 3) & ~3)) x[t] = v;
+    y[t] = 0;
+    __syncthreads();
+    if (t < N) {
+      int larger = 0;
+      const ulonglong2* x2 = reinterpret_cast<const ulonglong2*>(x);
+#pragma unroll 4
+      for (int i = 0; i < (N + 3) / 4 * 2; ++i) {
+        const ulonglong2 o = x2[i];
+        larger += (o.x > v) + (o.y > v);
+      }
+      y[larger] = v;
+    }
+    __syncthreads();
+    return y[t];
+  }
+  for (int size = 2; size <= THREADS; size <<= 1) {
+    for (int stride = size >> 1; stride > 0; stride >>= 1) {
+      unsigned long long o;
+      if (stride >= 32) {
+        x[t] = v;
+        __syncthreads();
+        o = x[t ^ stride];
+        unsigned long long* z = x;
+        x = y;
+        y = z;
+      } else {
+        o = __shfl_xor_sync(0xffffffffu, v, stride);
+      }
+      const bool larger = ((t & size) == 0) == ((t & stride) == 0);
+      v = larger == (o > v) ? o : v;
+    }
+  }
+  return v;
+}
+
+// a / b rounded to float32 but for some 2^-30 of it; 0 < b, a <= b. (In float64 it takes longer
+// than all else that follows a draw.)
+__device__ __forceinline__ float quotient_of(unsigned long long a, unsigned long long b) {
+  const float ah = __ull2float_rn(a), bh = __ull2float_rn(b);  // and what they leave, exact
+  const float al = static_cast<float>(static_cast<long long>(a - __float2ull_rn(ah)));
+  const float bl = static_cast<float>(static_cast<long long>(b - __float2ull_rn(bh)));
+  const float q = __fdiv_rn(ah, bh);
+  return q + __fdiv_rn(__fmaf_rn(-q, bh, ah) + __fmaf_rn(-q, bl, al), bh);
+}
+
 // A border in the order (l descending, j ascending): entries with a larger key, and the
 // first `ties` (by index) of those with this key.
 struct Border {
@@ -349,7 +404,7 @@ __device__ __noinline__ void slow_row(const SampleFilteredArgs& a, int row, cons
   if (t == 0) {
     const int j = s_pick >= 0 ? s_pick : top;
     a.tokens[row] = a.ids ? a.ids[j] : j;
-    if (a.probs) a.probs[row] = static_cast<float>(static_cast<double>(s_pickw) / static_cast<double>(total));
+    if (a.probs) a.probs[row] = total ? quotient_of(s_pickw, total) : 0.f;
   }
 }
 
@@ -433,12 +488,19 @@ __device__ __forceinline__ float largest(const uint4& v) {
     return fmaxf(__low2float(a), __high2float(a));
   }
 }
-// Logit e of 16 bytes of them; -0 becomes 0.
+// Logit e of 16 bytes of them.
 template <typename T>
 __device__ __forceinline__ float logit_of(const uint4& v, int e) {
   const uint32_t x[4] = {v.x, v.y, v.z, v.w};
-  return (sizeof(T) == 4 ? __uint_as_float(x[e & 3])
-                         : __uint_as_float(e & 1 ? x[e >> 1] & 0xffff0000u : x[e >> 1] << 16)) + 0.f;
+  return sizeof(T) == 4 ? __uint_as_float(x[e & 3])
+                        : __uint_as_float(e & 1 ? x[e >> 1] & 0xffff0000u : x[e >> 1] << 16);
+}
+// The same where e is not known to the compiler; -0 becomes 0.
+template <typename T>
+__device__ __forceinline__ float pick(const uint4& v, int e) {
+  const int word = e / (4 / static_cast<int>(sizeof(T)));
+  const uint32_t x = word < 2 ? (word == 0 ? v.x : v.y) : (word == 2 ? v.z : v.w);
+  return (sizeof(T) == 4 ? __uint_as_float(x) : __uint_as_float(e & 1 ? x & 0xffff0000u : x << 16)) + 0.f;
 }
 
 // What every CTA of a row does next, decided by the first one.
@@ -462,7 +524,7 @@ struct RowSmem {
   unsigned long long mass[kTopBins];  // and, for top-p alone, masses of the top bins
   uint32_t cc[kBins];                 // first CTA: the row's counts up to and including a bin
   float cm[kBins];                    // and masses (estimated from the counts below the top bins)
-  unsigned long long ent[THREADS];    // listed entries: order_key << 32 | ~index
+  alignas(16) unsigned long long ent[THREADS];  // listed entries: order_key << 32 | ~index
   unsigned long long sorted[THREADS];
   unsigned long long red[32], seg[THREADS / 32], all[kMaxCluster * (THREADS / 32)];
   unsigned long long own[2];          // this CTA's mass; its mass of x < xa
@@ -526,10 +588,9 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
       if (l >= cut && l <= past) hits |= 1u << e;
     }
     while (hits) {
-      const int e = __ffs(hits) - 1, word = e / (VEC / 4);
+      const int e = __ffs(hits) - 1;
       hits &= hits - 1;
-      const uint32_t x = word < 2 ? (word == 0 ? v.x : v.y) : (word == 2 ? v.z : v.w);
-      f(e, (sizeof(T) == 4 ? __uint_as_float(x) : __uint_as_float(e & 1 ? x & 0xffff0000u : x << 16)) + 0.f);
+      f(e, pick<T>(v, e));
     }
   };
 
@@ -589,20 +650,18 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
         atomicAdd(&S.cnt[static_cast<int>(pl)], 1u);
       }
       __syncthreads();
-      if (t < 32) {  // the first bin down to which k of them lie
-        uint32_t h[kBins / 32], s = 0;
+      if (t < 32) {  // the first bin down to which k of them lie (the last, if there are fewer)
+        static_assert(kBins == 1024, "32 bins a lane");
+        uint32_t s = 0;
 #pragma unroll
-        for (int i = 0; i < kBins / 32; ++i) s += h[i] = S.cnt[lane * (kBins / 32) + i];
-        const uint32_t in = warp_incl(s);
-        const unsigned who = __ballot_sync(0xffffffffu, in >= static_cast<uint32_t>(k));
-        if (lane == (who ? __ffs(who) - 1 : 31)) {
-          uint32_t before = in - s;
-          int bin = 0;
-#pragma unroll
-          for (int i = 0; i < kBins / 32 - 1; ++i)
-            if (bin == i && before + h[i] < static_cast<uint32_t>(k)) before += h[i], ++bin;
-          S.bin = lane * (kBins / 32) + bin;
-        }
+        for (int i = 0; i < 32; ++i) s += S.cnt[lane * 32 + ((i + lane) & 31)];  // a bank each
+        uint32_t in = warp_incl(s);
+        unsigned who = __ballot_sync(0xffffffffu, in >= static_cast<uint32_t>(k));
+        const int at = who ? __ffs(who) - 1 : 31;
+        const uint32_t before = __shfl_sync(0xffffffffu, in - s, at);
+        in = before + warp_incl(S.cnt[at * 32 + lane]);
+        who = __ballot_sync(0xffffffffu, in >= static_cast<uint32_t>(k));
+        if (lane == 0) S.bin = at * 32 + (who ? __ffs(who) - 1 : 31);
       }
       __syncthreads();
       const float end = fminf(static_cast<float>(S.bin + 1), kLastBin);
@@ -685,12 +744,11 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
   auto logit_at = [&](float y) { return m < INFINITY ? m - (y + 0.01f) / per * 1.00001f - fabsf(m) * 1e-6f : m; };
   // and above this, one before `y`
   auto logit_from = [&](float y) { return y > 0.f ? m - (y - 0.01f) / per * 0.99999f + fabsf(m) * 1e-6f : m; };
-  // exp((l - m) / T) 2^shift by ex2, its argument in two parts too: a slope off by a rounding
+  // exp(-d / T) 2^shift (d = m - l) by ex2, its argument in two parts too: a slope off by a rounding
   // would tilt the whole tail
-  auto ex2_at = [&](float l, float shift) {
-    const float d = __fsub_rn(l, m);
+  auto ex2_of = [&](float d, float shift) {
     float e;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(__fmaf_rn(d, c.hi, __fmaf_rn(d, c.lo, shift))));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(__fmaf_rn(d, -c.hi, __fmaf_rn(d, -c.lo, shift))));
     return e;
   };
   // The weight of a logit at place pl. Those that are kept whatever the border (`summed`, many)
@@ -698,12 +756,12 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
   // weight in a segment's sum and in its walk.
   auto weight = [&](float l, float pl, bool summed) -> unsigned long long {
     if (!summed || pl < kTopBins) return weight_fix<kExact>(l, m, c, S.tab);
-    return pl < kLastBin ? __float2ull_rn(ex2_at(l, static_cast<float>(kFixBits))) : 0;
+    return pl < kLastBin ? __float2ull_rn(ex2_of(__fsub_rn(m, l), static_cast<float>(kFixBits))) : 0;
   };
   auto key_weight = [&](uint32_t key) { return weight_fix<kExact>(key_value(key), m, c, S.tab); };
   const bool plain = m < INFINITY && per > 0.f && per < INFINITY;  // no 0 times infinity in a place
   auto ratio = [&](float l, unsigned long long sum) {  // the probability of a drawn logit
-    return static_cast<float>(static_cast<double>(weight_fix<kExact>(l, m, c, S.tab)) / static_cast<double>(sum));
+    return sum ? quotient_of(weight_fix<kExact>(l, m, c, S.tab), sum) : 0.f;
   };
   const unsigned long long least = least_weight(mp);
   const bool whole_list = V <= kList;
@@ -721,36 +779,63 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
       });
     }
   };
+  // The passes' inner loop: f(entry, its place) for a vector's entries, with no branch, and the
+  // weights of those from the top bins' end up to `end`, by ex2, added to `low`; then g(entry,
+  // logit, place) for the others of a place below `past`, few.
+  auto straight = [&](const uint4& v, float end, float past, float& low, auto f, auto g) {
+    uint32_t others = 0;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      const float d = __fsub_rn(m, logit_of<T>(v, e)), pl = __fmul_rn(d, per);
+      f(e, pl);
+      const bool in = pl >= kTopBins && pl < end;
+      const float w = ex2_of(d, 0.f);
+      low += in ? w : 0.f;
+      if (!in && pl < past) others |= 1u << e;
+    }
+    while (others) {
+      const int e = __ffs(others) - 1;
+      others &= others - 1;
+      const float l = pick<T>(v, e);
+      g(e, l, __fmul_rn(__fsub_rn(m, l), per));
+    }
+  };
+  // (A place's bin by an addition: conversions take 8 cycles a warp.)
+  auto count_place = [&](float pl, float end) {
+    if (pl < end) atomicAdd(&S.cnt[__float_as_uint(__fadd_rz(pl, 8388608.f)) & (kBins - 1)], 1u);  // not a NaN
+  };
   // Counts all bins of the first window; for top-p alone (kWeigh) also sums the slice's mass and
   // the top bins' masses.
   auto count_all = [&](auto weigh) {
     constexpr bool kWeigh = decltype(weigh)::value;
     unsigned long long sum = 0;
     float low = 0.f;
-    auto one = [&](float l, float pl) {
-      if (pl < kLastBin) {  // not a NaN
-        atomicAdd(&S.cnt[static_cast<int>(pl)], 1u);
-        if constexpr (kWeigh) {
-          if (pl < kTopBins) {
-            const unsigned long long w = weight(l, pl, true);
-            atomicAdd(&S.mass[static_cast<int>(pl)], w);
-            sum += w;
-          } else {
-            low += ex2_at(l, 0.f);
-          }
-        }
-      }
+    auto weigh_top = [&](float l, float pl) {
+      const unsigned long long w = weight(l, pl, true);
+      atomicAdd(&S.mass[static_cast<int>(pl)], w);
+      sum += w;
     };
     for (int i = t; i < nvec; i += THREADS) {
       const uint4 v = load(i);
       if (plain) {
+        if constexpr (kWeigh) {
+          straight(v, kLastBin, kTopBins, low, [&](int, float pl) { count_place(pl, kLastBin); },
+                   [&](int, float l, float pl) { weigh_top(l, pl); });
+        } else {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          const float l = logit_of<T>(v, e);
-          one(l, __fmul_rn(__fsub_rn(m, l), per));
+          for (int e = 0; e < VEC; ++e) count_place(__fmul_rn(__fsub_rn(m, logit_of<T>(v, e)), per), kLastBin);
         }
       } else {
-        each_between(v, -INFINITY, INFINITY, [&](int, float l) { one(l, place(l)); });
+        each_between(v, -INFINITY, INFINITY, [&](int, float l) {
+          const float pl = place(l);
+          count_place(pl, kLastBin);
+          if constexpr (kWeigh) {
+            if (pl < kTopBins)
+              weigh_top(l, pl);
+            else if (pl < kLastBin)
+              low += ex2_of(__fsub_rn(m, l), 0.f);
+          }
+        });
       }
     }
     if constexpr (kWeigh) {
@@ -831,11 +916,12 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
     cmd.early = cmd.ties = cmd.fresh = 0;
     if (B == kBins) B = last;  // all that has weight, or a mass estimated too low
     B = first ? max(first_least, min(B, first_most)) : max(at_least, min(B, at_most));
+    const int most = min(last, first ? first_most : at_most);  // no border past it
     cmd.what = kPass;
     const uint32_t before = B ? S.cc[B - 1] : base_count, here = S.cc[B] - before;
     if (S.cc[B] <= kList) {  // everything down to the border fits
       int hi = B;
-      if (!count_left && hi < last && S.cc[hi + 1] <= kList) ++hi;
+      if (!count_left && hi < most && S.cc[hi + 1] <= kList) ++hi;
       cmd.xa = 0.f;
       cmd.xb = cmd.x0 + (hi + 1) / cmd.scale;
       above_count = 0;
@@ -846,7 +932,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
         cmd.ties = 1;  // within 2^(1/22528) of one another: equal logits
       } else if (!count_left) {  // the masses are estimates: take the neighbours too where they fit
         if (lo > 0 && S.cc[hi] - (lo > 1 ? S.cc[lo - 2] : base_count) <= kList) --lo;
-        if (hi < last && S.cc[hi + 1] - (lo > 0 ? S.cc[lo - 1] : base_count) <= kList) ++hi;
+        if (hi < most && S.cc[hi + 1] - (lo > 0 ? S.cc[lo - 1] : base_count) <= kList) ++hi;
       }
       cmd.xa = cmd.x0 + lo / cmd.scale;
       cmd.xb = cmd.x0 + (hi + 1) / cmd.scale;
@@ -907,106 +993,99 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
         cmd = choose(cmd);
       }
     } else {
-     if (!all_listed) {
-      // ---- one pass: sum what is kept anyhow (per warp's segment), list the rest
-      __syncthreads();
-      if (t == 0) S.n_list = 0, S.kmin = 0xffffffffu, S.kmax = 0;
-      __syncthreads();
-      unsigned long long kept = 0, all = 0;
-      uint32_t tied = 0, kmin = 0xffffffffu, kmax = 0;
-      const float xa = cmd.xa, xb = fminf(cmd.xb, kLastBin), cut = logit_at(xb);
-      auto list = [&](int j, float l) {  // of the zone
-        const uint32_t key = order_key(l);
-        if (cmd.ties) {
-          ++tied;
-          kmin = min(kmin, key);
-          kmax = max(kmax, key);
-        } else {
-          const uint32_t pos = atomicAdd(&S.n_list, 1u);
-          if (pos < kList) S.ent[pos] = (static_cast<unsigned long long>(key) << 32) | ~static_cast<uint32_t>(j);
-        }
-      };
-      const int v0 = warp * seg_vecs + lane, v1 = (warp + 1) * seg_vecs;
-      if (xa > 0.f && plain && least == 0) {
-        // Small weights are added up in float32 per thread: a segment's sum is then off by some
-        // 2^-24 of it, which moves a draw by less than the weights' own error.
-        const float xa1 = fminf(xa, kLastBin);
-        float low = 0.f;
-        for (int i = v0; i < v1; i += 32) {
-          const uint4 q = load(i);
-          if (largest<T>(q) < cut) continue;
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            const float l = logit_of<T>(q, e);
-            const float pl = __fmul_rn(__fsub_rn(m, l), per);
-            if (pl < xa1) {
-              if (pl < kTopBins)
+      if (!all_listed) {
+        // ---- one pass: sum what is kept anyhow (per warp's segment), list the rest
+        __syncthreads();
+        if (t == 0) S.n_list = 0, S.kmin = 0xffffffffu, S.kmax = 0;
+        __syncthreads();
+        unsigned long long kept = 0, all = 0;
+        uint32_t tied = 0, kmin = 0xffffffffu, kmax = 0;
+        const float xa = cmd.xa, xb = fminf(cmd.xb, kLastBin), cut = logit_at(xb);
+        auto list = [&](int j, float l) {  // of the zone
+          const uint32_t key = order_key(l);
+          if (cmd.ties) {
+            ++tied;
+            kmin = min(kmin, key);
+            kmax = max(kmax, key);
+          } else {
+            const uint32_t pos = atomicAdd(&S.n_list, 1u);
+            if (pos < kList) S.ent[pos] = (static_cast<unsigned long long>(key) << 32) | ~static_cast<uint32_t>(j);
+          }
+        };
+        const int v0 = warp * seg_vecs + lane, v1 = (warp + 1) * seg_vecs;
+        if (xa > 0.f && plain && least == 0) {
+          // Small weights are added up in float32 per thread: a segment's sum is then off by some
+          // 2^-24 of it, which moves a draw by less than the weights' own error.
+          const float xa1 = fminf(xa, kLastBin);
+          float low = 0.f;
+          for (int i = v0; i < v1; i += 32) {
+            const uint4 q = load(i);
+            if (largest<T>(q) < cut) continue;
+            straight(q, xa1, xb, low, [](int, float) {}, [&](int e, float l, float pl) {
+              if (pl < xa1)
                 kept += weight(l, pl, true);
               else
-                low += ex2_at(l, 0.f);
-            } else if (pl < xb) {
-              list(j0 + i * VEC + e, l);
-            }
+                list(j0 + i * VEC + e, l);
+            });
+          }
+          kept += __float2ull_rn(low * static_cast<float>(1ull << kFixBits));
+          all = kept;
+        } else if (xa > 0.f) {
+          for (int i = v0; i < v1; i += 32) {
+            const uint4 q = load(i);
+            if (largest<T>(q) < cut) continue;
+            each_between(q, cut, INFINITY, [&](int e, float l) {
+              const float pl = place(l);
+              if (pl < xa && pl < kLastBin) {
+                const unsigned long long w = weight(l, pl, true);
+                all += w;
+                if (w >= least) kept += w;
+              } else if (pl < xb) {
+                list(j0 + i * VEC + e, l);
+              }
+            });
+          }
+        } else {
+          for (int i = v0; i < v1; i += 32) {
+            const uint4 q = load(i);
+            if (largest<T>(q) < cut) continue;
+            each_between(q, cut, INFINITY, [&](int e, float l) {
+              if (place(l) < xb) list(j0 + i * VEC + e, l);
+            });
           }
         }
-        kept += __float2ull_rn(low * static_cast<float>(1ull << kFixBits));
-        all = kept;
-      } else if (xa > 0.f) {
-        for (int i = v0; i < v1; i += 32) {
-          const uint4 q = load(i);
-          if (largest<T>(q) < cut) continue;
-          each_between(q, cut, INFINITY, [&](int e, float l) {
-            const float pl = place(l);
-            if (pl < xa && pl < kLastBin) {
-              const unsigned long long w = weight(l, pl, true);
-              all += w;
-              if (w >= least) kept += w;
-            } else if (pl < xb) {
-              list(j0 + i * VEC + e, l);
-            }
-          });
-        }
-      } else {
-        for (int i = v0; i < v1; i += 32) {
-          const uint4 q = load(i);
-          if (largest<T>(q) < cut) continue;
-          each_between(q, cut, INFINITY, [&](int e, float l) {
-            if (place(l) < xb) list(j0 + i * VEC + e, l);
-          });
-        }
-      }
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        kept += __shfl_xor_sync(0xffffffffu, kept, o);
-        all += __shfl_xor_sync(0xffffffffu, all, o);
-        tied += __shfl_xor_sync(0xffffffffu, tied, o);
-      }
-      if (cmd.ties && kmax) {
-        atomicMin(&S.kmin, kmin);
-        atomicMax(&S.kmax, kmax);
-      }
-      if (lane == 0) {
-        S.seg[warp] = kept;
-        S.segties[warp] = tied;
-        S.red[warp] = all;
-      }
-      __syncthreads();
-      if (t == 0) {
-        unsigned long long s = 0;
-        for (int w = 0; w < NW; ++w) s += S.red[w];
-        S.own[1] = s;
-      }
-      if (t < C) {
-        if (C > 1) {
-          peer_store(&S.found[rank], t, S.n_list);
-          peer_store(&S.key_min[rank], t, S.kmin);
-          peer_store(&S.key_max[rank], t, S.kmax);
-        } else {
-          S.found[0] = S.n_list, S.key_min[0] = S.kmin, S.key_max[0] = S.kmax;
+        for (int o = 16; o > 0; o >>= 1) {
+          kept += __shfl_xor_sync(0xffffffffu, kept, o);
+          all += __shfl_xor_sync(0xffffffffu, all, o);
+          tied += __shfl_xor_sync(0xffffffffu, tied, o);
         }
+        if (cmd.ties && kmax) {
+          atomicMin(&S.kmin, kmin);
+          atomicMax(&S.kmax, kmax);
+        }
+        if (lane == 0) {
+          S.seg[warp] = kept;
+          S.segties[warp] = tied;
+          S.red[warp] = all;
+        }
+        __syncthreads();
+        if (t == 0) {
+          unsigned long long s = 0;
+          for (int w = 0; w < NW; ++w) s += S.red[w];
+          S.own[1] = s;
+        }
+        if (t < C) {
+          if (C > 1) {
+            peer_store(&S.found[rank], t, S.n_list);
+            peer_store(&S.key_min[rank], t, S.kmin);
+            peer_store(&S.key_max[rank], t, S.kmax);
+          } else {
+            S.found[0] = S.n_list, S.key_min[0] = S.kmin, S.key_max[0] = S.kmax;
+          }
+        }
+        row_sync(C);
       }
-      row_sync(C);
-     }
       const bool early = cmd.early;
       if (early && rank != 0) {  // the first CTA goes on alone once it has read the lists
         row_arrive(C);
@@ -1015,7 +1094,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
       }
       if (rank == 0) {
         // ---- the border and the draw
-        const unsigned long long above = row_total(&S.own[1]);
+        const unsigned long long above = cmd.xa > 0.f ? row_total(&S.own[1]) : 0;
         uint32_t start[kMaxCluster + 1], lo_key = 0xffffffffu, hi_key = 0;
         start[0] = 0;
 #pragma unroll
@@ -1037,17 +1116,10 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
           for (int i = t; i < C * NW; i += THREADS) S.all[i] = C > 1 ? peer_load(&S.seg[i % NW], i / NW) : S.seg[i];
         if (early) row_arrive(C);  // lists read
         __syncthreads();
-        // sorted by counting the larger entries
-        if (t < N) S.ent[t] = ent;
+        ent = sort_down<THREADS>(ent, N, S.ent, S.sorted);
         __syncthreads();
-        if (t < N) {
-          int larger = 0;
-          for (int i = 0; i < N; ++i) larger += S.ent[i] > ent;
-          S.sorted[larger] = ent;
-        }
-        __syncthreads();
+        S.sorted[t] = ent;
         // entry t in order: its weight, and the weights up to and including it
-        ent = t < N ? S.sorted[t] : 0;
         const unsigned long long w = t < N ? key_weight(static_cast<uint32_t>(ent >> 32)) : 0;
         auto scan = [&](unsigned long long v) {  // inclusive over the block
           const unsigned long long in = warp_incl(v);
@@ -1112,6 +1184,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
           cmd.what = kSlow;
         } else if (again == 2) {
           if (cmd.scale == 1.f) {
+            first_most = static_cast<int>(cmd.xb) - 1;  // top-p's border is no further
             cmd = choose(cmd);
           } else {  // back to the first window
             cmd.what = kCount, cmd.fresh = 1, cmd.x0 = 0.f, cmd.scale = 1.f, cmd.b0 = 0, cmd.b1 = kLastBin;
@@ -1148,21 +1221,21 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
           // the kept entries in index order: the draw is the first whose sum passes it
           const uint32_t idx = ~static_cast<uint32_t>(ent);
           const unsigned long long wk = t < static_cast<int>(keep) && w >= least ? w : 0;
+          // (~index << 32 | place in the other order, largest first)
+          unsigned long long by = t < static_cast<int>(keep) ? static_cast<unsigned long long>(~idx) << 32 | t : 0;
           __syncthreads();
-          if (t < static_cast<int>(keep)) S.ent[t] = idx;
+          by = sort_down<THREADS>(by, static_cast<int>(keep), S.ent, S.sorted);
           __syncthreads();
-          int pos = 0;
-          if (t < static_cast<int>(keep))
-            for (int i = 0; i < static_cast<int>(keep); ++i) pos += static_cast<uint32_t>(S.ent[i]) < idx;
-          if (t < static_cast<int>(keep)) S.sorted[pos] = wk;
+          S.ent[t] = wk;
+          S.sorted[t] = ent;
           __syncthreads();
-          const unsigned long long v = t < static_cast<int>(keep) ? S.sorted[t] : 0, in = scan(v);
-          if (t == static_cast<int>(keep) - 1) S.left = in;
+          const int at = static_cast<int>(by & (THREADS - 1));
+          const unsigned long long v = t < static_cast<int>(keep) ? S.ent[at] : 0, in = scan(v);
+          if (t == THREADS - 1) S.left = in;
           __syncthreads();
           const unsigned long long sum = S.left, draw = floor_part(u, sum);
-          if (in > draw && in - v <= draw) S.pick = t;
-          __syncthreads();
-          if (t < static_cast<int>(keep) && pos == static_cast<int>(S.pick)) emit(idx, ratio(key_value(static_cast<uint32_t>(ent >> 32)), sum));
+          if (in > draw && in - v <= draw)
+            emit(static_cast<int>(~static_cast<uint32_t>(by >> 32)), ratio(key_value(static_cast<uint32_t>(S.sorted[at] >> 32)), sum));
           cmd.what = kDone;
         } else {
           // the kept masses of the row's segments, and the one the draw falls in
