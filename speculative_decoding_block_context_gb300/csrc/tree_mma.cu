@@ -160,6 +160,27 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
+// Two float32 operations an instruction.
+__device__ __forceinline__ unsigned long long pack2(float x, float y) {
+  unsigned long long d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(x), "f"(y));
+  return d;
+}
+__device__ __forceinline__ float2 unpack2(unsigned long long x) {
+  float2 d;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(x));
+  return d;
+}
+__device__ __forceinline__ unsigned long long fma2(unsigned long long x, unsigned long long a, unsigned long long b) {
+  unsigned long long d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(x), "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ unsigned long long add2(unsigned long long x, unsigned long long y) {
+  unsigned long long d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(x), "l"(y));
+  return d;
+}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -547,22 +568,24 @@ __global__ void __launch_bounds__(MmaCfg<HD, MT>::THREADS, 1)
             mx = to;
           }
           const float base = mx == -INFINITY ? 0.f : mx;
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          const unsigned long long scale2 = pack2(k2, k2), base2 = pack2(-base, -base);
+          unsigned long long sum[2] = {0, 0};
 #pragma unroll
           for (int x = 0; x < TN; x += 32) {
             uint32_t p[16];
 #pragma unroll
             for (int y = 0; y < 16; ++y) {
-              const float e0 = ex2(fmaf(__uint_as_float(s[x + 2 * y]), k2, -base));
-              const float e1 = ex2(fmaf(__uint_as_float(s[x + 2 * y + 1]), k2, -base));
-              sum[y & 1] += e0;
-              sum[2 + (y & 1)] += e1;
+              const float2 z = unpack2(
+                  fma2(pack2(__uint_as_float(s[x + 2 * y]), __uint_as_float(s[x + 2 * y + 1])), scale2, base2));
+              const float e0 = ex2(z.x), e1 = ex2(z.y);
+              sum[y & 1] = add2(sum[y & 1], pack2(e0, e1));
               const __nv_bfloat162 b2 = __floats2bfloat162_rn(e0, e1);
               p[y] = *reinterpret_cast<const uint32_t*>(&b2);
             }
             tmem_st16(s_addr + x / 2, p);
           }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          const float2 sums = unpack2(add2(sum[0], sum[1]));
+          l += sums.x + sums.y;
           tmem_wait_st();
         }
         ++n;
