@@ -68,7 +68,7 @@ __global__ void __launch_bounds__(256) tree_simt_kernel(const TreeAttnArgs a) {
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   unsigned err = 0;
   Spot spot;
-  const Share share = locate<C::THREADS, TM, TN>(a, 1, spot, err, red, &s_spot);
+  const Share share = locate<C::THREADS, TM, TN, 1, 0>(a, spot, err, red, &s_spot);
   Walk<TM, TN> w(a, share, spot);
   const float k2 = a.scale * 1.4426950408889634f;
   int tree_b = -1;

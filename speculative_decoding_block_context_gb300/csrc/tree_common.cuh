@@ -46,21 +46,27 @@ __device__ __forceinline__ int64_t quotient(int64_t x, int y) {
   return x / y;
 }
 
-// T units over `ctas` CTAs; CTA c takes units [begin(c), begin(c + 1)), begin(c) = floor(T c / ctas).
+// The share out of a batch's units. Evenly: CTA c takes units [begin(c), begin(c + 1)) of T,
+// begin(c) = floor(T c / ctas), and may so end one item and begin the next. Or, with few items,
+// `cut` position tiles of one item each: an item's count is rounded up to a multiple of it.
 struct Share {
   int64_t T;
-  int ctas;
-  __device__ Share(int64_t units, int grid, int least) : T(units) {
+  int ctas, cut;  // cut 0: evenly
+  __device__ Share(int64_t units, int grid, int least) : T(units), cut(0) {
     // no CTA with fewer than `least` units (but one): shorter shares cost more in partial
     // sums than they save
     ctas = static_cast<int>(max(static_cast<int64_t>(1), min(static_cast<int64_t>(grid), quotient(T, least))));
   }
   __device__ int64_t begin(int c) const {
+    if (cut) return static_cast<int64_t>(cut) * c;
     const int64_t q = quotient(T, ctas);
     const int r = static_cast<int>(T - q * ctas);
     return q * c + static_cast<uint32_t>(r * c) / static_cast<uint32_t>(ctas);  // r c < ctas^2
   }
 };
+__device__ __forceinline__ int rounded_up(int nt, int cut) {
+  return cut ? static_cast<int>(static_cast<uint32_t>(nt + cut - 1) / static_cast<uint32_t>(cut)) * cut : nt;
+}
 
 struct Spot {
   int b;         // the request that holds the unit
@@ -92,9 +98,11 @@ __device__ __forceinline__ int64_t unit_scan(int64_t v, int64_t* red, int64_t& t
 }
 
 // The batch's share out, and the request of CTA blockIdx.x's first unit (b = bs when it has
-// none). Called by the whole block; every thread gets the answer.
-template <int THREADS, int TM, int TN>
-__device__ __forceinline__ Share locate(const TreeAttnArgs& a, int least, Spot& spot, unsigned& err, int64_t* red,
+// none). Called by the whole block; every thread gets the answer. A CTA's second item costs it
+// as much as kItemTiles more position tiles (0: evenly at all events): where one item for each CTA costs fewer, they
+// have one each (a tree of 16 nodes over 2048 positions: 20.2 us evenly, 15.7 so).
+template <int THREADS, int TM, int TN, int kLeast, int kItemTiles>
+__device__ __forceinline__ Share locate(const TreeAttnArgs& a, Spot& spot, unsigned& err, int64_t* red,
                                         Spot* shared_spot) {
   const int t = threadIdx.x;
   int64_t T = 0, mine = 0, incl = 0;
@@ -111,8 +119,20 @@ __device__ __forceinline__ Share locate(const TreeAttnArgs& a, int least, Spot& 
   }
   if (t == 0) *shared_spot = Spot{a.bs, 0, {0, 0, 0}};
   __syncthreads();
-  const Share share(T, gridDim.x, least);
-  const int64_t u = static_cast<int>(blockIdx.x) < share.ctas ? share.begin(blockIdx.x) : T;
+  Share share(T, gridDim.x, kLeast);
+  const int64_t items = static_cast<int64_t>(a.bs) * a.nkv * ((a.width * a.group + TM - 1) / TM), grid = gridDim.x;
+  if (kItemTiles > 0 && T > 0 && 2 * items <= grid) {  // (so bs <= THREADS)
+    const int64_t each = max(static_cast<int64_t>(kLeast), quotient(T - 1, static_cast<int>(grid - items)) + 1);
+    if (each <= quotient(T - 1, share.ctas) + 1 + kItemTiles) {
+      share.cut = static_cast<int>(each);  // at most T / cut + items <= grid CTAs
+      mine = r.n > 0 ? static_cast<int64_t>(a.nkv) * Cut<TM, TN>::row_tiles(a, r) *
+                           rounded_up(Cut<TM, TN>::pos_tiles(r), share.cut)
+                     : 0;
+      incl = unit_scan<THREADS>(mine, red, share.T);
+      share.ctas = static_cast<int>(quotient(share.T, share.cut));
+    }
+  }
+  const int64_t u = static_cast<int>(blockIdx.x) < share.ctas ? share.begin(blockIdx.x) : share.T;
   if (t < a.bs && incl - mine <= u && u < incl) *shared_spot = Spot{t, incl - mine, r};
   if (a.bs > THREADS) {  // the unit may lie past the first chunk
     int64_t before = 0;
@@ -153,6 +173,12 @@ struct Walk {
     const int c = blockIdx.x;
     if (c < share.ctas && s.b < a.bs) u = share.begin(c), u1 = share.begin(c + 1);
     enter(a);
+    if (share.cut && u < u1) {  // units that are there: from here on no item is rounded up
+      const int up = rounded_up(nt, share.cut);
+      const int64_t g = quotient(u - base, up);
+      u += g * (nt - up);
+      u1 = min(u1 + g * (nt - up), base + (g + 1) * nt);
+    }
   }
   // The next item; false when the range is done.
   __device__ bool next(const TreeAttnArgs& a) {
@@ -193,7 +219,10 @@ __device__ __forceinline__ void write_join_task(const TreeAttnArgs& a, const Sha
   if (w.started && w.t0 == 0 && w.t1 < w.nt) {
     const int64_t end = w.u + (w.nt - w.t1);  // one past the row tile's last unit
     int last = blockIdx.x + 1;
-    while (last + 1 < share.ctas && share.begin(last + 1) < end) ++last;
+    if (share.cut)
+      last += (w.nt - w.t1 - 1) / share.cut;
+    else
+      while (last + 1 < share.ctas && share.begin(last + 1) < end) ++last;
     task = JoinTask{w.b, w.head, w.tile_m, min(TM, w.r.n * a.group - w.tile_m * TM),
                     static_cast<int>(2 * blockIdx.x) + (w.first_item ? 0 : 1), last};
   }

@@ -43,7 +43,8 @@ struct MmaCfg {
 // TMEM columns: S (and then P) of lane m, buffer i at 128 m + 64 i; the lane's O at 256 + 128 m
 __device__ __forceinline__ constexpr uint32_t s_col(int m, int i) { return static_cast<uint32_t>(128 * m + 64 * i); }
 __device__ __forceinline__ constexpr uint32_t o_col(int m) { return static_cast<uint32_t>(256 + 128 * m); }
-constexpr int kLeastTiles = 4;  // position tiles a CTA takes at least
+constexpr int kLeastTiles = 3;  // position tiles a CTA takes at least
+constexpr int kItemTiles = 6;   // what a CTA's second item costs, in position tiles (8 single tokens over 1000 positions: 21.1 us at 3, 19.5 at 6)
 constexpr int kRing = 64;  // position tiles whose readable blocks are remembered
 constexpr int kTmemCols = 512;
 
@@ -259,7 +260,7 @@ __global__ void __launch_bounds__(MmaCfg<HD, MT>::THREADS, 1)
 
   unsigned err = 0;
   Spot spot;
-  const Share share = locate<C::THREADS, TM, TN>(a, kLeastTiles, spot, err, red, &s_spot);
+  const Share share = locate<C::THREADS, TM, TN, kLeastTiles, kItemTiles>(a, spot, err, red, &s_spot);
   Walk<TM, TN> w(a, share, spot);
   volatile int* ab = &abort_flag;
   // the item's rows, and whether each lane has rows of its own
