@@ -478,12 +478,15 @@ flashmap_status flashmap_tree_attention_workspace(const flashmap_cache_layer* ca
  *   workspace    (device, 256-byte aligned) flashmap_tree_attention_workspace bytes; its
  *                contents do not matter, one call at a time may use it
  * Scores, the softmax and its sums are float32; with BF16 the probabilities are rounded to
- * bf16 for their product with the values. Cached keys and values of visible positions must
- * be finite or give NaN; positions past a request's last node are not read into results.
+ * bf16 for their product with the values. A key hidden from a node does not reach its
+ * output; the values of all positions up to the request's last node must be finite (a hidden
+ * one's weight is 0, and 0 times one that is not is NaN). Positions past the last node are
+ * not read into results.
  * Device checks: a page id out of range or a position past the table's stride hides the
  * position (PAGE, POSITION); a request with a bad table row or negative ctx_lens is skipped
  * (REQUEST, POSITION), its rows of out left as they were; a node whose id names no earlier
- * node sees the context and itself (TREE); a row that sees nothing is 0. Limits: width <=
+ * node sees the context and itself (TREE); a row that sees nothing is 0. A load that has not
+ * come in a second ends the call with what it has (TIMEOUT). Limits: width <=
  * 1025, num_heads a multiple of num_kv_heads, num_pages * num_kv_heads * page_size < 2^31.
  */
 flashmap_status flashmap_tree_attention(const flashmap_cache_layer* cache, const void* q, int64_t q_stride,
@@ -505,8 +508,8 @@ flashmap_status flashmap_tree_attention(const flashmap_cache_layer* cache, const
  * temperature <= 0 (or NaN) takes the largest logit, the lowest index on ties. Logits of
  * -inf or NaN are never drawn; a row of nothing else gives index 0 with probability 0.
  * The weights are taken as multiples of 2^-44 (an entry whose weight rounds to none is never
- * drawn, even at u = 0) and summed exactly: a row's token does not depend on the other rows,
- * the launch or the order of the sums.
+ * drawn, even at u = 0), good to about 1e-9 where they decide a filter's border and to 2^-22
+ * where small ones are only added up. The same call draws the same tokens.
  *   logits      (device) [rows] rows of vocab F32 or BF16 entries, ld entries apart
  *   temperature (device) float32, top_k int32, top_p, min_p float32, per request; the last
  *               three may be NULL: off
@@ -516,7 +519,8 @@ flashmap_status flashmap_tree_attention(const flashmap_cache_layer* cache, const
  *   tokens_out  (device) int64 [rows]
  *   probs_out   (device) float32 [rows] the token's probability among the kept entries (1
  *               when greedy), or NULL
- * Limits: vocab <= 393216.
+ * A row whose logits could not be loaded in a second gets token -1 with probability 0.
+ * Limits: vocab <= 393216, rows <= 2^27.
  */
 flashmap_status flashmap_sample_filtered(const void* logits, int32_t dtype, int32_t rows, int32_t vocab, int64_t ld,
                                          int32_t rows_per_request, const float* temperature, const int32_t* top_k,

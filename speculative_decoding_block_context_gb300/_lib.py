@@ -180,14 +180,23 @@ def _stream(stream):
     return _vp(torch.cuda.current_stream().cuda_stream)
 
 
-def _here(stream, t):
-    """The stream handle as an integer, the one given or torch's current one; t must be on the current device."""
+def _device(t) -> int:
+    """The current device, which t must be on."""
     import torch
 
+    if not t.is_cuda:
+        raise ValueError(f"the tensors must be on the GPU, got {t.device}")
     device = torch._C._cuda_getDevice()
     if t.get_device() != device:
         raise ValueError(f"the tensors are on {t.device}, the current device is cuda:{device}")
-    return stream if stream is not None else torch._C._cuda_getCurrentRawStream(device)
+    return device
+
+
+def _handle(stream, device: int):
+    """The stream handle as an integer: the one given, or torch's current one."""
+    import torch
+
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
 
 
 def make_config(d: dict) -> flashmap_config:
@@ -336,17 +345,17 @@ def _dtypes() -> dict:
     return _DT
 
 
-def _bad(name: str, t, dtype, n: int):
-    raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor of at least {n} elements, got "
-                     f"{tuple(t.shape)} {t.dtype} on {t.device}")
+def _bad(name: str, t, dtype, n: int, device: int):
+    raise ValueError(f"{name} must be a contiguous {dtype} tensor of at least {n} elements on the current device "
+                     f"(cuda:{device}), got {tuple(t.shape)} {t.dtype} on {t.device}")
 
 
-def _dense(name: str, t, dtype, n: int = 0):
-    """The pointer of t (None for None), checked: contiguous, on the GPU, this dtype, n elements at least."""
+def _dense(device: int, name: str, t, dtype, n: int = 0):
+    """The pointer of t (None for None), checked: contiguous, on this GPU, this dtype, n elements at least."""
     if t is None:
         return None
-    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous() or t.numel() < n:
-        _bad(name, t, dtype, n)
+    if t.dtype is not dtype or t.get_device() != device or not t.is_contiguous() or t.numel() < n:
+        _bad(name, t, dtype, n, device)
     return t.data_ptr()
 
 
@@ -354,21 +363,21 @@ def flashmap_extend_pages(req_pool_idx, lens, new_lens, held, page_size: int, re
                           free_head_out, held_out, num_pages: int, cu_tokens, slots, positions=None, token_req=None,
                           dev_err=None, stream=None) -> None:
     """Extends req_to_page (rows, stride) in place; slots' length is the most tokens a call may have."""
-    dt = _dtypes()
+    dt, on = _dtypes(), _device(slots)
     i32, i64 = dt["i32"], dt["i64"]
     bs, most = req_pool_idx.numel(), slots.numel()
     if req_to_page.dim() != 2:
         raise ValueError("req_to_page must be (rows, stride)")
     rows, stride = req_to_page.shape
     _check(lib().flashmap_extend_pages(
-        bs, _dense("req_pool_idx", req_pool_idx, i32), _dense("lens", lens, i32, bs),
-        _dense("new_lens", new_lens, i32, bs), _dense("held", held, i32, bs), page_size,
-        _dense("req_to_page", req_to_page, i32), rows, stride, _dense("free_pages", free_pages, i32),
-        free_pages.numel(), _dense("free_head", free_head, i32, 1),
-        _dense("free_head_out", free_head_out, i32, 1), _dense("held_out", held_out, i32, bs), num_pages, most,
-        _dense("cu_tokens", cu_tokens, i32, bs + 1), _dense("slots", slots, i64),
-        _dense("positions", positions, i32, most), _dense("token_req", token_req, i32, most),
-        _dense("dev_err", dev_err, i32, 1), _here(stream, slots)))
+        bs, _dense(on, "req_pool_idx", req_pool_idx, i32), _dense(on, "lens", lens, i32, bs),
+        _dense(on, "new_lens", new_lens, i32, bs), _dense(on, "held", held, i32, bs), page_size,
+        _dense(on, "req_to_page", req_to_page, i32), rows, stride, _dense(on, "free_pages", free_pages, i32),
+        free_pages.numel(), _dense(on, "free_head", free_head, i32, 1),
+        _dense(on, "free_head_out", free_head_out, i32, 1), _dense(on, "held_out", held_out, i32, bs), num_pages, most,
+        _dense(on, "cu_tokens", cu_tokens, i32, bs + 1), _dense(on, "slots", slots, i64),
+        _dense(on, "positions", positions, i32, most), _dense(on, "token_req", token_req, i32, most),
+        _dense(on, "dev_err", dev_err, i32, 1), _handle(stream, on)))
 
 
 def make_cache_layer(keys, values) -> flashmap_cache_layer:
@@ -377,10 +386,11 @@ def make_cache_layer(keys, values) -> flashmap_cache_layer:
     kind = keys.dtype
     if keys.dim() != 4 or keys.shape != values.shape or kind not in (f32, bf16):
         raise ValueError("keys and values must be float32 or bfloat16 (num_pages, num_kv_heads, page_size, head_dim)")
+    on = max(0, keys.get_device())
     pages, heads, page, hd = keys.shape
-    c = flashmap_cache_layer(_dense("keys", keys, kind), _dense("values", values, kind), pages, heads, page, hd,
+    c = flashmap_cache_layer(_dense(on, "keys", keys, kind), _dense(on, "values", values, kind), pages, heads, page, hd,
                              F32 if kind is f32 else BF16)
-    c.kind, c._keep = kind, (keys, values)
+    c.kind, c.device, c._keep = kind, on, (keys, values)
     return c
 
 
@@ -394,46 +404,49 @@ def flashmap_tree_attention(cache: flashmap_cache_layer, q, width: int, ctx_lens
                             req_to_page, scale: float, out, workspace, dev_err=None, stream=None) -> None:
     """q (bs * width, num_heads, head_dim), its rows possibly further apart (a slice of a wider
     projection); out the same shape, contiguous; tree_ids (bs, width - 1) from flashmap_build_tree or None."""
-    dt = _dtypes()
+    dt, on = _dtypes(), _device(q)
     i32, i64 = dt["i32"], dt["i64"]
     bs = ctx_lens.numel()
     n, heads, hd = q.shape
     step, head_step, one = q.stride()
-    if q.dtype is not cache.kind or not q.is_cuda or n != bs * width or hd != cache.head_dim or one != 1 or \
+    if q.dtype is not cache.kind or cache.device != on or n != bs * width or hd != cache.head_dim or one != 1 or \
             (head_step != hd and heads > 1):
-        raise ValueError("q must be (bs * width, num_heads, head_dim) in the cache's dtype with dense rows")
+        raise ValueError("q must be (bs * width, num_heads, head_dim) in the cache's dtype with dense rows, "
+                         "on the current device as the cache is")
     if req_to_page.dim() != 2:
         raise ValueError("req_to_page must be (rows, stride)")
     rows, stride = req_to_page.shape
+    if workspace.get_device() != on or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the current device")
     _check(lib().flashmap_tree_attention(
         _c.byref(cache), q.data_ptr(), step if n > 1 else heads * hd, bs, width, heads,
-        _dense("ctx_lens", ctx_lens, i32), _dense("num_nodes", num_nodes, i32, bs),
-        _dense("tree_ids", tree_ids, i64, bs * (width - 1)), _dense("req_pool_idx", req_pool_idx, i32, bs),
-        _dense("req_to_page", req_to_page, i32), rows, stride, scale,
-        _dense("out", out, cache.kind, bs * width * heads * hd), workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _dense("dev_err", dev_err, i32, 1), _here(stream, q)))
+        _dense(on, "ctx_lens", ctx_lens, i32), _dense(on, "num_nodes", num_nodes, i32, bs),
+        _dense(on, "tree_ids", tree_ids, i64, bs * (width - 1)), _dense(on, "req_pool_idx", req_pool_idx, i32, bs),
+        _dense(on, "req_to_page", req_to_page, i32), rows, stride, scale,
+        _dense(on, "out", out, cache.kind, bs * width * heads * hd), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _dense(on, "dev_err", dev_err, i32, 1), _handle(stream, on)))
 
 
 def flashmap_sample_filtered(logits, rows_per_request: int, temperature, top_k, top_p, min_p, uniforms, ids,
                              tokens_out, probs_out=None, stream=None) -> None:
     """logits (rows, vocab) float32 or bfloat16, rows possibly further apart than vocab; top_k, top_p,
     min_p, ids and probs_out may be None."""
-    dt = _dtypes()
+    dt, on = _dtypes(), _device(logits)
     i32, i64, f32 = dt["i32"], dt["i64"], dt["f32"]
     kind = logits.dtype
-    if logits.dim() != 2 or not logits.is_cuda or kind not in (f32, dt["bf16"]) or \
+    if logits.dim() != 2 or kind not in (f32, dt["bf16"]) or \
             (logits.stride(1) != 1 and logits.shape[1] > 1):
-        raise ValueError("logits must be a CUDA float32 or bfloat16 (rows, vocab) tensor with dense rows")
+        raise ValueError("logits must be a float32 or bfloat16 (rows, vocab) tensor with dense rows")
     rows, vocab = logits.shape
     bs = -(-rows // max(1, rows_per_request))
     _check(lib().flashmap_sample_filtered(
         logits.data_ptr(), F32 if kind is f32 else BF16, rows, vocab,
         logits.stride(0) if rows > 1 else vocab,
-        rows_per_request, _dense("temperature", temperature, f32, bs), _dense("top_k", top_k, i32, bs),
-        _dense("top_p", top_p, f32, bs), _dense("min_p", min_p, f32, bs),
-        _dense("uniforms", uniforms, f32, rows), _dense("ids", ids, i64, vocab),
-        _dense("tokens_out", tokens_out, i64, rows), _dense("probs_out", probs_out, f32, rows),
-        _here(stream, logits)))
+        rows_per_request, _dense(on, "temperature", temperature, f32, bs), _dense(on, "top_k", top_k, i32, bs),
+        _dense(on, "top_p", top_p, f32, bs), _dense(on, "min_p", min_p, f32, bs),
+        _dense(on, "uniforms", uniforms, f32, rows), _dense(on, "ids", ids, i64, vocab),
+        _dense(on, "tokens_out", tokens_out, i64, rows), _dense(on, "probs_out", probs_out, f32, rows),
+        _handle(stream, on)))
 
 
 def flashmap_get_device_error(model: Model, stream=None) -> int:

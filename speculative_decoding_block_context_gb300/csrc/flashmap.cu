@@ -1611,6 +1611,7 @@ flashmap_status flashmap_sample_filtered(const void* logits, int32_t dtype, int3
   if (rows <= 0 || vocab <= 0 || rows_per_request <= 0) return fail(FLASHMAP_E_INVALID, "every size must be positive");
   if (ld < vocab) return fail(FLASHMAP_E_INVALID, "ld must be at least vocab");
   if (vocab > fm::kSampleFilteredMaxVocab) return fail(FLASHMAP_E_UNSUPPORTED, "vocab must be <= 393216");
+  if (rows > 1 << 27) return fail(FLASHMAP_E_UNSUPPORTED, "rows must be <= 2^27");  // up to 8 CTAs each
   if (reinterpret_cast<uintptr_t>(logits) % dt_size(dtype)) return fail(FLASHMAP_E_INVALID, "logits are misaligned");
   Launch L{};
   if (const flashmap_status st = current_launch(stream, nullptr, &L)) return st;

@@ -8,7 +8,8 @@
 //
 // Which entry a border or a draw falls on must not hang on rounding, so weights are
 // integers: w 2^44 rounded, from an exponential good to about 1e-9, summed exactly in
-// 64 bits in whatever order.
+// 64 bits in whatever order. Two exceptions, where many small ones are only added up (see
+// `weight` and the passes): there ex2 (2^-22) and float32 sums per thread will do.
 //
 // A row is held in the shared memory of a cluster of CTAs, so that it is read from memory
 // once. Its entries are counted in bins of x = (m - l) * 22 log2(e) / T, 22 bins per
@@ -77,7 +78,7 @@ __device__ __forceinline__ Slope slope_of(float T) {
   return s;
 }
 
-// exp((l - m) / T) 2^44, rounded. With x = (l - m) log2(e) / T carried in two parts,
+// exp((l - m) / T) 2^44, rounded, by the table-driven method of P. T. P. Tang (1989). With x = (l - m) log2(e) / T carried in two parts,
 // x = n / 32 + r, |r| <= 1/64: 2^x = 2^(n / 32) (1 + (2^r - 1)), the first factor from a
 // table of 32 values in two parts and the second's excess from four terms of its series
 // (the fifth is below 4e-13). The mantissa is put together as an integer and shifted.
@@ -464,8 +465,8 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                "l"(src), "r"(bytes), "r"(smem_u32(bar))
                : "memory");
 }
-// Waits for a bulk copy; the clock is looked at only every 256 tries.
-__device__ __forceinline__ void landed(uint64_t* bar, volatile int* gave_up) {
+// Waits for a bulk copy (false: in vain); the clock is looked at only every 256 tries.
+__device__ __forceinline__ bool landed(uint64_t* bar, volatile int* gave_up) {
   uint64_t t0 = 0;
   for (uint32_t i = 1; !mbar_try_wait(bar, 0); ++i) {
     if (i & 255) continue;
@@ -473,9 +474,10 @@ __device__ __forceinline__ void landed(uint64_t* bar, volatile int* gave_up) {
     if (t0 == 0) t0 = now;
     if (*gave_up || now - t0 > kWaitLimitNs) {
       *gave_up = 1;
-      return;
+      return false;
     }
   }
+  return true;
 }
 // The largest of 16 bytes of logits (NaN aside).
 template <typename T>
@@ -619,7 +621,10 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
     for (int i = whole_vecs * VEC + t; i < slice; i += THREADS) sl[i] = i < n ? lr[j0 + i] : from_f32<T>(-INFINITY);
     __syncthreads();
     for (int q = 0; q * chunk < nvec; ++q) {
-      if (q * chunk < whole_vecs) landed(&S.landed[q], &S.gave_up);
+      if (q * chunk < whole_vecs && !landed(&S.landed[q], &S.gave_up) && t == 0) {
+        int again = 0;  // a copy in flight lands before its CTA's shared memory goes
+        landed(&S.landed[q], &again);
+      }
       for (int i = q * chunk + t; i < min(nvec, (q + 1) * chunk); i += THREADS) see(i, load(i));
     }
   } else {
@@ -640,6 +645,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
   const bool by_count = k < V, by_mass = p < 1.f, by_mass_only = by_mass && !by_count;
   float slice_top = -INFINITY;
   for (int w = 0; w < NW; ++w) slice_top = fmaxf(slice_top, __uint_as_float(static_cast<uint32_t>(S.red[w])));
+  if (S.gave_up) slice_top = NAN;  // tells the row's CTAs
   // A small top-k needs no counting: where k threads' largest logits lie, at least k logits
   // do, and few more. Each slice lists its own down to there, before the row's maximum is known.
   const bool quick = by_count && k <= kQuick && !greedy;
@@ -695,7 +701,11 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
   }
   row_sync(C);
   float m = -INFINITY;
-  for (int r = 0; r < C; ++r) m = fmaxf(m, __uint_as_float(S.top[r]));
+  bool lost = false;
+  for (int r = 0; r < C; ++r) {
+    m = fmaxf(m, __uint_as_float(S.top[r]));
+    lost |= isnan(__uint_as_float(S.top[r]));
+  }
   m += 0.f;  // -0 counts as 0
   auto row_total = [&](const auto* x) {  // of the same variable of every CTA, all loads in flight
     auto s = *x;
@@ -713,6 +723,13 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
     a.tokens[row] = a.ids ? a.ids[j] : j;
     if (a.probs) a.probs[row] = prob;
   };
+  if (lost) {
+    if (rank == 0 && t == 0) {
+      a.tokens[row] = -1;
+      if (a.probs) a.probs[row] = 0.f;
+    }
+    return;
+  }
   if (!(m > -INFINITY)) {  // nothing to draw
     if (rank == 0 && t == 0) emit(0, 0.f);
     return;

@@ -528,3 +528,220 @@ def test_verify_a_drafted_tree(dtype):
     c.check(out.cpu())
     check_sampling(logits, width, params["temp"], params["k"], params["p"], params["mp"], u.tolist())
     assert held_out.tolist() == [3, 1, 6, 2, 2] and int(head) == at + 4
+
+
+# ------------------------------------------------------------------ how they are called
+
+
+def cuda_case(c):
+    """A case's tensors on the GPU, as the call takes them (the workspace aside)."""
+    cache = F.make_cache_layer(c.keys.cuda(), c.values.cuda())
+    return dict(cache=cache, q=c.q.cuda(), width=c.width, ctx=i32(c.ctx), nodes=i32(c.nodes) if c.nodes else None,
+                ids=c.ids.cuda() if c.ids is not None else None, req=c.req.cuda(), table=c.table.cuda(), scale=c.scale)
+
+
+def attend(d, out, ws, err=None, stream=None):
+    F.flashmap_tree_attention(d["cache"], d["q"], d["width"], d["ctx"], d["nodes"], d["ids"], d["req"], d["table"],
+                              d["scale"], out, ws, err, stream)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", [
+    (17, 17, 10, 5, 64, 32, [37 * i * i % 2999 for i in range(17)], [1 + i for i in range(17)], False),  # shares end inside items
+    (16, 3, 8, 4, 64, 16, [2900 + i for i in range(16)], None, True),
+    (2, 9, 8, 2, 128, 16, [1500, 40], None, True),       # each item cut apart
+    (3, 5, 4, 2, 64, 16, [0, 900, 64], [0, 5, 0], True),  # two of three requests without nodes
+    (4, 33, 8, 2, 64, 16, [10, 0, 511, 700], [33, 1, 32, 17], True),  # one or two row tiles
+], ids=["even", "even long", "cut", "cut, empty", "cut, ragged"])
+def test_tree_attention_shares(shape, dtype):
+    bs, width, heads, kv, hd, P, ctx, nodes, ids = shape
+    c = Case(bs, width, heads, kv, hd, P, ctx, nodes, ids, dtype, seed=bs)
+    out, err = c.run()
+    assert err == 0
+    c.check(out)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_tree_attention_a_hidden_key_does_not_matter(dtype):
+    """NaN and infinite keys in nodes: the rows that do not see them are as they were."""
+    c = Case(2, 10, 8, 2, 64, 16, [70, 20], None, True, dtype, seed=11)
+    a, _ = c.run()
+    hit = {0: 7, 1: 4}
+    for b, i in hit.items():
+        pos = c.ctx[b] + i
+        c.keys[c.table[c.req[b], pos // 16], :, pos % 16] = float("nan") if b else float("inf")
+    z, err = c.run()
+    assert err == 0
+    for b, i in hit.items():
+        parent = ref.parents_of(c.ids[b].tolist(), 10)
+        for node in range(10):
+            x, seen = node, False
+            while x >= 0:
+                seen |= x == i
+                x = parent[x]
+            if not seen:
+                assert torch.equal(a[b * 10 + node], z[b * 10 + node]), (b, node)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_tree_attention_refuses_workspaces(dtype):
+    c = Case(1, 4, 4, 2, 64, 16, [100], None, True, dtype)
+    d = cuda_case(c)
+    n = F.flashmap_tree_attention_workspace(d["cache"], 1, 4, 4)
+    out = torch.full(c.q.shape, 7.0, dtype=c.q.dtype, device="cuda")
+    ws = torch.zeros(n + 256, dtype=torch.uint8, device="cuda")
+    for bad in (ws[: n - 1], ws[16:], ws[:0]):
+        with pytest.raises((F.FlashmapError, ValueError)):
+            attend(d, out, bad)
+    with pytest.raises((F.FlashmapError, ValueError, TypeError)):
+        attend(d, out, torch.zeros(n, dtype=torch.uint8))
+    torch.cuda.synchronize()
+    assert (out == 7.0).all()
+    attend(d, out, ws[:n])
+    c.check(out.cpu())
+
+
+def test_tree_attention_graphs_share_a_workspace():
+    """Two captured calls of different shapes over one workspace, replayed in turn."""
+    cases = [Case(3, 16, 8, 2, 128, 16, [900, 5, 4000], None, True, "bf16", seed=1),
+             Case(2, 40, 8, 2, 128, 16, [3000, 77], [40, 9], True, "bf16", seed=2)]
+    ds = [cuda_case(c) for c in cases]
+    ws = torch.full((max(F.flashmap_tree_attention_workspace(d["cache"], c.bs, c.width, 8) for c, d in zip(cases, ds)),),
+                    255, dtype=torch.uint8, device="cuda")
+    outs = [torch.full(c.q.shape, 7.0, dtype=c.q.dtype, device="cuda") for c in cases]
+    graphs, s = [], torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for d, out in zip(ds, outs):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            attend(d, out, ws)
+        graphs.append(graph)
+    for _ in range(3):
+        for out in outs:
+            out.fill_(7.0)
+        for graph in graphs:
+            graph.replay()
+        torch.cuda.synchronize()
+        for c, out in zip(cases, outs):
+            c.check(out.cpu())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_calls_on_two_streams(dtype):
+    """Calls at once, each with a workspace and outputs of its own."""
+    c = Case(8, 8, 8, 2, 64, 16, [300 * i for i in range(8)], None, True, dtype, seed=3)
+    d = cuda_case(c)
+    alone, _ = c.run()
+    V = 50257
+    g = torch.Generator(device="cuda").manual_seed(3)
+    logits = 2.5 * torch.randn((8, V), generator=g, device="cuda")
+    f = lambda x: torch.full((8,), x, device="cuda")  # noqa: E731
+    u = torch.rand(8, generator=g, device="cuda")
+    args = (f(0.9), i32([0, 40] * 4), f(0.9), f(0.0), u, None)
+    want = torch.empty(8, dtype=torch.int64, device="cuda")
+    F.flashmap_sample_filtered(logits, 1, *args, want, None)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    n = F.flashmap_tree_attention_workspace(d["cache"], 8, 8, 8)
+    sets = [(torch.zeros(n, dtype=torch.uint8, device="cuda"), torch.full(c.q.shape, 7.0, dtype=c.q.dtype, device="cuda"),
+             torch.empty(8, dtype=torch.int64, device="cuda")) for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s, (ws, out, tokens) in zip(streams, sets):
+            with torch.cuda.stream(s):
+                attend(d, out, ws)
+                F.flashmap_sample_filtered(logits, 1, *args, tokens, None)
+    torch.cuda.synchronize()
+    for _, out, tokens in sets:
+        assert torch.equal(out.cpu(), alone) and torch.equal(tokens, want)
+
+
+def test_pages_and_sampling_replay():
+    """Captured once, replayed with other inputs in the same buffers."""
+    P, bs = 16, 3
+    req, lens, new, held = i32([2, 0, 1]), i32([0, 0, 0]), i32([1, 1, 1]), i32([0, 0, 0])
+    start = torch.arange(40, dtype=torch.int32, device="cuda").reshape(5, 8)
+    table, free, head, out_head = start.clone(), i32(list(range(50, 70))), i32([0]), i32([-1])
+    cu, slots, err = i32([0] * 4), torch.zeros(64, dtype=torch.int64, device="cuda"), i32([0])
+    V = 9000
+    g = torch.Generator(device="cuda").manual_seed(8)
+    logits = torch.zeros((bs, V), device="cuda")
+    temp, k, p, u = torch.ones(bs, device="cuda"), i32([0] * bs), torch.ones(bs, device="cuda"), torch.zeros(bs, device="cuda")
+    tokens, probs = torch.zeros(bs, dtype=torch.int64, device="cuda"), torch.zeros(bs, device="cuda")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        F.flashmap_extend_pages(req, lens, new, held, P, table, free, head, out_head, None, 70, cu, slots, None, None, err)
+        F.flashmap_sample_filtered(logits, 1, temp, k, p, None, u, None, tokens, probs)
+    for seed in range(2):
+        r = np.random.default_rng(seed)
+        a, n = [int(x) for x in r.integers(0, 60, bs)], [int(x) for x in r.integers(0, 20, bs)]
+        h = [-(-x // P) for x in a]
+        for x, y in ((lens, a), (new, n), (held, h)):
+            x.copy_(i32(y))
+        table.copy_(start)
+        slots.fill_(-9)
+        logits.copy_(2.5 * torch.randn((bs, V), generator=g, device="cuda"))
+        k.copy_(i32([0, 30, 700]))
+        p.fill_(0.9)
+        u.copy_(torch.rand(bs, generator=g, device="cuda"))
+        graph.replay()
+        torch.cuda.synchronize()
+        t, hd, _, c, want, *_ = ref.extend_pages([2, 0, 1], a, n, h, P, start.cpu().numpy(), list(range(50, 70)), 0, 70, 64)
+        np.testing.assert_array_equal(table.cpu().numpy(), t)
+        assert int(err) == 0 and int(out_head) == hd
+        np.testing.assert_array_equal(slots.cpu().numpy()[: c[-1]], want[: c[-1]])
+        again = run_sampling(logits, 1, [1.0] * 3, [0, 30, 700], [0.9] * 3, None, u.tolist())
+        np.testing.assert_array_equal(tokens.cpu().numpy(), again[0])
+        np.testing.assert_array_equal(probs.cpu().numpy(), again[1])
+        check_sampling(logits, 1, [1.0] * 3, [0, 30, 700], [0.9] * 3, None, u.tolist())
+
+
+# ------------------------------------------------------------------ far offsets
+
+
+def test_pages_far_ids():
+    """Slots past 2^31."""
+    free = [(1 << 30) - 7, 1 << 29, (1 << 30) - 1]
+    err, served = check_pages([0, 1], [0, 16], [20, 1], [0, 1], 16, [[-1] * 4, [(1 << 30) - 2] + [-1] * 3], free, 0,
+                              1 << 30, 64)
+    assert err == 0 and all(served)
+
+
+@pytest.mark.parametrize("dtype,hd", [("bf16", 128), ("bf16", 64), ("f32", 32)])
+def test_tree_attention_far_pages(dtype, hd):
+    """Pages whose entries lie past 2^31 elements give what the same pages give near the start."""
+    kv, P = 8, 16
+    c = Case(2, 6, 16, kv, hd, P, [200, 33], None, True, dtype, seed=4)
+    near, _ = c.run()
+    few = c.keys.shape[0]
+    pages = (1 << 31) // (kv * P * hd) + few + 5
+    dt = c.q.dtype
+    keys, values = (torch.empty((pages, kv, P, hd), dtype=dt, device="cuda") for _ in range(2))
+    keys[pages - few:] = c.keys.cuda()
+    values[pages - few:] = c.values.cuda()
+    d = cuda_case(c)
+    d["cache"] = F.make_cache_layer(keys, values)
+    d["table"] = torch.where(d["table"] >= 0, d["table"] + (pages - few), d["table"])
+    out = torch.full(c.q.shape, 7.0, dtype=dt, device="cuda")
+    ws = torch.zeros(F.flashmap_tree_attention_workspace(d["cache"], 2, 6, 16), dtype=torch.uint8, device="cuda")
+    attend(d, out, ws)
+    torch.cuda.synchronize()
+    assert torch.equal(out.cpu(), near)
+
+
+def test_sampling_far_and_many_rows():
+    V, rows, ld = 1000, 9, 1 << 28
+    g = torch.Generator(device="cuda").manual_seed(6)
+    few = (2.5 * torch.randn((rows, V), generator=g, device="cuda")).bfloat16()
+    u = torch.rand(rows, generator=g, device="cuda").tolist()
+    want = run_sampling(few, 3, [0.9] * 3, [0, 20, 0], [0.9, 1.0, 1.0], None, u)
+    far = torch.empty(((rows - 1) * ld + V,), dtype=torch.bfloat16, device="cuda").as_strided((rows, V), (ld, 1))
+    far.copy_(few)
+    got = run_sampling(far, 3, [0.9] * 3, [0, 20, 0], [0.9, 1.0, 1.0], None, u)
+    np.testing.assert_array_equal(got[0], want[0])
+    np.testing.assert_array_equal(got[1], want[1])
+    del far
+    times = 8000
+    got = run_sampling(few.repeat(times, 1), 3, [0.9] * 3 * times, [0, 20, 0] * times, [0.9, 1.0, 1.0] * times, None,
+                       u * times)
+    np.testing.assert_array_equal(got[0].reshape(times, rows), np.tile(want[0], (times, 1)))

@@ -83,7 +83,7 @@ def test_tree_attention_workspace_refuses(lib):
 
 @pytest.mark.parametrize("change,status", [
     (dict(logits=None), 1), (dict(temp=None), 1), (dict(u=None), 1), (dict(tokens=None), 1), (dict(dtype=F.E4M3), 1),
-    (dict(rows=0), 1), (dict(vocab=0), 1), (dict(per=0), 1), (dict(ld=9), 1), (dict(vocab=393217, ld=393217), 2),
+    (dict(rows=0), 1), (dict(vocab=0), 1), (dict(per=0), 1), (dict(ld=9), 1), (dict(vocab=393217, ld=393217), 2), (dict(rows=(1 << 27) + 1), 2),
     (dict(logits=A + 1), 1)])
 def test_sample_filtered_refuses(lib, change, status):
     d = dict(logits=A, dtype=F.F32, rows=2, vocab=10, ld=10, per=1, temp=A, k=None, p=None, mp=None, u=A, ids=None,
