@@ -182,11 +182,9 @@ def _stream(stream):
 
 def _device(t) -> int:
     """The current device, which t must be on."""
-    import torch
-
     if not t.is_cuda:
         raise ValueError(f"the tensors must be on the GPU, got {t.device}")
-    device = torch._C._cuda_getDevice()
+    device = _DT["device"]()
     if t.get_device() != device:
         raise ValueError(f"the tensors are on {t.device}, the current device is cuda:{device}")
     return device
@@ -194,9 +192,7 @@ def _device(t) -> int:
 
 def _handle(stream, device: int):
     """The stream handle as an integer: the one given, or torch's current one."""
-    import torch
-
-    return torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
+    return _DT["stream"](device) if stream is None else _stream(stream)
 
 
 def make_config(d: dict) -> flashmap_config:
@@ -334,14 +330,15 @@ def flashmap_build_tree(candidates, width: int, tokens_out, ids_out, stats_out, 
                                      _ptr(ids_out), _ptr(stats_out), _stream(stream)))
 
 
-_DT = {}  # torch dtypes by short name, filled once
+_DT = {}  # torch dtypes by short name, and how it tells the current device and stream, filled once
 
 
 def _dtypes() -> dict:
     if not _DT:
         import torch
 
-        _DT.update(i32=torch.int32, i64=torch.int64, f32=torch.float32, bf16=torch.bfloat16)
+        _DT.update(i32=torch.int32, i64=torch.int64, f32=torch.float32, bf16=torch.bfloat16,
+                   device=torch._C._cuda_getDevice, stream=torch._C._cuda_getCurrentRawStream)
     return _DT
 
 
