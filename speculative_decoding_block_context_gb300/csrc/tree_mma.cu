@@ -462,12 +462,15 @@ __global__ void __launch_bounds__(MmaCfg<HD, MT>::THREADS, 1)
     struct Query {
       uint4 v[HD / 8];
     };
+    auto q_of = [&](const Rows& q) {
+      return reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + q.q_row * a.q_stride +
+                                            static_cast<int64_t>(q.head) * HD);
+    };
     auto ask = [&](const Rows& q, Query& qv) {
 #pragma unroll
       for (int x = 0; x < HD / 8; ++x) qv.v[x] = make_uint4(0, 0, 0, 0);
       if (!q.loads || !q.live) return;
-      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + q.q_row * a.q_stride +
-                                                        static_cast<int64_t>(q.head) * HD);
+      const uint4* src = q_of(q);
 #pragma unroll
       for (int x = 0; x < HD / 8; ++x) qv.v[x] = __ldcg(src + x);
     };
@@ -512,6 +515,18 @@ __global__ void __launch_bounds__(MmaCfg<HD, MT>::THREADS, 1)
       const int node = q.node, seq0 = seq;
       seq += w.t1 - w.t0;
       const int first = w.t0 + (own ? 0 : m), step = own ? 1 : 2;
+      // The next item is looked up while this one's first scores run.
+      Walk<TM, TN> w2 = w;
+      more = w2.next(a);
+      Rows q2{};
+      if (more) {
+        q2 = rows_for(w2);
+        if (q2.loads && q2.live) {
+          const char* src = reinterpret_cast<const char*>(q_of(q2));
+#pragma unroll
+          for (int x = 0; x < HD * 2; x += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + x));
+        }
+      }
       float mx = -INFINITY, l = 0.f;  // the maximum the weights are taken against, and their sum
       for (int t = first; t < w.t1; t += step) {
         const int p0 = t * TN, buf = n & 1;
@@ -598,11 +613,7 @@ __global__ void __launch_bounds__(MmaCfg<HD, MT>::THREADS, 1)
       const int tiles1 = own ? w.t1 - w.t0 : (w.t1 - w.t0) / 2;  // lane 1's tiles of the item
       // The next item's queries go in before this one's output comes out: its first scores run
       // meanwhile.
-      Walk<TM, TN> w2 = w;
-      more = w2.next(a);
-      Rows q2{};
       Query qv;
-      if (more) q2 = rows_for(w2);
       ask(q2, qv);
       if (!own && m == 1) {
         if (tiles1 > 0) {  // lane 0 joins the two outputs
