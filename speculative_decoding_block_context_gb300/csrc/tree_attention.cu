@@ -6,8 +6,8 @@
 // A request's nodes and a key/value head's group of query heads make n * group query rows
 // that read the same keys, so they share one pass over them. The work is cut into units
 // (request, key/value head, row tile, position tile), in that order, and CTA c of G takes
-// units [T c / G, T (c + 1) / G): every CTA streams the same number of tiles whatever the
-// requests' lengths. T hangs on lengths that only the device knows, so each CTA sums the
+// units [T c / G, T (c + 1) / G): every CTA streams about the same number of tiles whatever
+// the requests' lengths. T hangs on lengths that only the device knows, so each CTA sums the
 // batch's units itself. A row tile that spans several CTAs leaves partial sums (running
 // maximum, sum and unnormalised output, float32) which a second kernel joins in CTA order.
 
@@ -68,7 +68,7 @@ __global__ void __launch_bounds__(256) tree_simt_kernel(const TreeAttnArgs a) {
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   unsigned err = 0;
   Spot spot;
-  const Share share = locate<C::THREADS, TM, TN, 1, 0>(a, spot, err, red, &s_spot);
+  const Share share = locate<C::THREADS, TM, TN, 1, 1>(a, spot, err, red, &s_spot);
   Walk<TM, TN> w(a, share, spot);
   const float k2 = a.scale * 1.4426950408889634f;
   int tree_b = -1;

@@ -35,8 +35,8 @@ template <int TM, int TN>
 struct Cut {
   __device__ static int row_tiles(const TreeAttnArgs& a, Request r) { return (r.n * a.group + TM - 1) / TM; }
   __device__ static int pos_tiles(Request r) { return (r.ctx + r.n + TN - 1) / TN; }
-  __device__ static int64_t units(const TreeAttnArgs& a, Request r) {
-    return r.n > 0 ? static_cast<int64_t>(a.nkv) * row_tiles(a, r) * pos_tiles(r) : 0;
+  __device__ static int64_t units(const TreeAttnArgs& a, Request r, int start) {
+    return r.n > 0 ? static_cast<int64_t>(a.nkv) * row_tiles(a, r) * (pos_tiles(r) + start) : 0;
   }
 };
 
@@ -46,13 +46,15 @@ __device__ __forceinline__ int64_t quotient(int64_t x, int y) {
   return x / y;
 }
 
-// The share out of a batch's units. Evenly: CTA c takes units [begin(c), begin(c + 1)) of T,
-// begin(c) = floor(T c / ctas), and may so end one item and begin the next. Or, with few items,
-// `cut` position tiles of one item each: an item's count is rounded up to a multiple of it.
+// The share out of a batch's units: an item's position tiles, and `start` units before them
+// for what beginning an item costs. Evenly: CTA c takes units [begin(c), begin(c + 1)) of T,
+// begin(c) = floor(T c / ctas), and may so end one item and begin the next (an end among an
+// item's first `start` units leaves that item to the next CTA). Or, with few items, `cut`
+// position tiles of one item each: an item's count is rounded up to a multiple of it.
 struct Share {
   int64_t T;
-  int ctas, cut;  // cut 0: evenly
-  __device__ Share(int64_t units, int grid, int least) : T(units), cut(0) {
+  int ctas, start, cut;  // cut 0: evenly
+  __device__ Share(int64_t units, int grid, int least, int start) : T(units), start(start), cut(0) {
     // no CTA with fewer than `least` units (but one): shorter shares cost more in partial
     // sums than they save
     ctas = static_cast<int>(max(static_cast<int64_t>(1), min(static_cast<int64_t>(grid), quotient(T, least))));
@@ -98,12 +100,17 @@ __device__ __forceinline__ int64_t unit_scan(int64_t v, int64_t* red, int64_t& t
 }
 
 // The batch's share out, and the request of CTA blockIdx.x's first unit (b = bs when it has
-// none). Called by the whole block; every thread gets the answer. A CTA's second item costs it
-// as much as kItemTiles more position tiles (0: evenly at all events): where one item for each CTA costs fewer, they
-// have one each (a tree of 16 nodes over 2048 positions: 20.2 us evenly, 15.7 so).
-template <int THREADS, int TM, int TN, int kLeast, int kItemTiles>
+// none). Called by the whole block; every thread gets the answer. An item costs a CTA as much
+// as kStart more position tiles: so they are counted (32 trees of 16 nodes over 512-8192
+// positions: 97 us, without 130), and where there are few items and one for each CTA costs
+// less than two for some, they have one each (a tree of 16 nodes over 2048 positions: 20.2 us
+// evenly, 15.4 so).
+template <int THREADS, int TM, int TN, int kLeast, int kStart>
 __device__ __forceinline__ Share locate(const TreeAttnArgs& a, Spot& spot, unsigned& err, int64_t* red,
                                         Spot* shared_spot) {
+  const int64_t items = static_cast<int64_t>(a.bs) * a.nkv * ((a.width * a.group + TM - 1) / TM), grid = gridDim.x;
+  const bool few = 2 * items <= grid;  // (so bs <= THREADS)
+  const int start = few ? 0 : kStart;
   const int t = threadIdx.x;
   int64_t T = 0, mine = 0, incl = 0;
   Request r{0, 0, 0};
@@ -111,7 +118,7 @@ __device__ __forceinline__ Share locate(const TreeAttnArgs& a, Spot& spot, unsig
     const int b = b0 + t;
     Request x{0, 0, 0};
     if (b < a.bs) x = request_of(a, b, err);
-    const int64_t v = Cut<TM, TN>::units(a, x);
+    const int64_t v = Cut<TM, TN>::units(a, x, start);
     int64_t chunk;
     const int64_t i = unit_scan<THREADS>(v, red, chunk);
     if (b0 == 0) mine = v, incl = i, r = x;
@@ -119,11 +126,10 @@ __device__ __forceinline__ Share locate(const TreeAttnArgs& a, Spot& spot, unsig
   }
   if (t == 0) *shared_spot = Spot{a.bs, 0, {0, 0, 0}};
   __syncthreads();
-  Share share(T, gridDim.x, kLeast);
-  const int64_t items = static_cast<int64_t>(a.bs) * a.nkv * ((a.width * a.group + TM - 1) / TM), grid = gridDim.x;
-  if (kItemTiles > 0 && T > 0 && 2 * items <= grid) {  // (so bs <= THREADS)
+  Share share(T, gridDim.x, kLeast, start);
+  if (few && T > 0) {
     const int64_t each = max(static_cast<int64_t>(kLeast), quotient(T - 1, static_cast<int>(grid - items)) + 1);
-    if (each <= quotient(T - 1, share.ctas) + 1 + kItemTiles) {
+    if (each <= quotient(T - 1, share.ctas) + 1 + kStart) {
       share.cut = static_cast<int>(each);  // at most T / cut + items <= grid CTAs
       mine = r.n > 0 ? static_cast<int64_t>(a.nkv) * Cut<TM, TN>::row_tiles(a, r) *
                            rounded_up(Cut<TM, TN>::pos_tiles(r), share.cut)
@@ -141,7 +147,7 @@ __device__ __forceinline__ Share locate(const TreeAttnArgs& a, Spot& spot, unsig
       const int b = b0 + t;
       Request x{0, 0, 0};
       if (b < a.bs) x = request_of(a, b, none);
-      const int64_t v = Cut<TM, TN>::units(a, x);
+      const int64_t v = Cut<TM, TN>::units(a, x, start);
       int64_t chunk;
       const int64_t i = before + unit_scan<THREADS>(v, red, chunk);
       if (b0 > 0 && b < a.bs && i - v <= u && u < i) *shared_spot = Spot{b, i - v, x};
@@ -160,6 +166,7 @@ struct Walk {
   int b;
   Request r;
   int nt, mt;                // position tiles and row tiles of the request
+  int start;                 // units before an item's position tiles
   int head, tile_m, t0, t1;  // the item: key/value head, row tile, its position tiles
   bool first_item, whole;    // the range's first item; it holds all of the row tile's positions
   bool started;
@@ -169,7 +176,7 @@ struct Walk {
     mt = Cut<TM, TN>::row_tiles(a, r);
   }
   __device__ Walk(const TreeAttnArgs& a, const Share& share, const Spot& s)
-      : u(0), u1(0), base(s.base), b(s.b), r(s.r), first_item(false), started(false) {
+      : u(0), u1(0), base(s.base), b(s.b), r(s.r), start(share.start), first_item(false), started(false) {
     const int c = blockIdx.x;
     if (c < share.ctas && s.b < a.bs) u = share.begin(c), u1 = share.begin(c + 1);
     enter(a);
@@ -182,23 +189,29 @@ struct Walk {
   }
   // The next item; false when the range is done.
   __device__ bool next(const TreeAttnArgs& a) {
-    if (u >= u1) return false;
-    while (r.n <= 0 || u - base >= static_cast<int64_t>(a.nkv) * mt * nt) {
-      base += r.n > 0 ? static_cast<int64_t>(a.nkv) * mt * nt : 0;
+    if (u1 - u <= (started ? start : 0)) return false;
+    while (r.n <= 0 || u - base >= static_cast<int64_t>(a.nkv) * mt * (nt + start)) {
+      base += r.n > 0 ? static_cast<int64_t>(a.nkv) * mt * (nt + start) : 0;
       unsigned none = 0;
       r = request_of(a, ++b, none);
       enter(a);
     }
     const int64_t local = u - base;
-    const int g = static_cast<int>(quotient(local, nt));
-    t0 = static_cast<int>(local - static_cast<int64_t>(g) * nt);
+    const int g = static_cast<int>(quotient(local, nt + start));
+    const int from = static_cast<int>(local - static_cast<int64_t>(g) * (nt + start));
+    const int to = static_cast<int>(min(static_cast<int64_t>(nt + start), from + (u1 - u)));
+    if (to <= start) {  // (the range's only item)
+      u = u1;
+      return false;
+    }
     head = g / mt;
     tile_m = g - head * mt;
-    t1 = static_cast<int>(min(static_cast<int64_t>(nt), t0 + (u1 - u)));
+    t0 = max(0, from - start);
+    t1 = to - start;
     first_item = !started;
     started = true;
     whole = t0 == 0 && t1 == nt;
-    u += t1 - t0;
+    u += to - from;
     return true;
   }
 };

@@ -44,7 +44,11 @@ struct MmaCfg {
 __device__ __forceinline__ constexpr uint32_t s_col(int m, int i) { return static_cast<uint32_t>(128 * m + 64 * i); }
 __device__ __forceinline__ constexpr uint32_t o_col(int m) { return static_cast<uint32_t>(256 + 128 * m); }
 constexpr int kLeastTiles = 3;  // position tiles a CTA takes at least
-constexpr int kItemTiles = 6;   // what a CTA's second item costs, in position tiles (8 single tokens over 1000 positions: 21.1 us at 3, 19.5 at 6)
+// What beginning an item costs, in position tiles, as the share out counts it. Measured: 128
+// trees of 64 nodes, heads of 128: 588 us at 6, 568 at 9, 538 at 14, 539 at 20, 565 at 40; 17
+// chains of 17 tokens, heads of 64: 18.1 at 6, 17.7 at 9, 19.2 at 14, 20.2 at 20.
+template <int HD>
+constexpr int kStartTiles = HD == 128 ? 14 : 9;
 constexpr int kRing = 64;  // position tiles whose readable blocks are remembered
 constexpr int kTmemCols = 512;
 
@@ -260,7 +264,7 @@ __global__ void __launch_bounds__(MmaCfg<HD, MT>::THREADS, 1)
 
   unsigned err = 0;
   Spot spot;
-  const Share share = locate<C::THREADS, TM, TN, kLeastTiles, kItemTiles>(a, spot, err, red, &s_spot);
+  const Share share = locate<C::THREADS, TM, TN, kLeastTiles, kStartTiles<HD>>(a, spot, err, red, &s_spot);
   Walk<TM, TN> w(a, share, spot);
   volatile int* ab = &abort_flag;
   // the item's rows, and whether each lane has rows of its own
