@@ -419,6 +419,7 @@ constexpr int kTopBins = 132;
 constexpr int kLastBin = 1014;       // from here on weights are 0
 constexpr int kMaxCluster = 8;
 constexpr int kChunks = 4;          // parts in which a slice is loaded
+constexpr int kSmallVocab = 2048;   // up to here many rows have 128 threads each
 constexpr int kQuick = 64;          // top-k up to this lists its candidates without counting
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -524,7 +525,7 @@ struct RowSmem {
   float2 tab[32];
   uint32_t cnt[kBins];                // this CTA's counts in the window's bins
   unsigned long long mass[kTopBins];  // and, for top-p alone, masses of the top bins
-  uint32_t cc[kBins];                 // first CTA: the row's counts up to and including a bin
+  alignas(8) uint32_t cc[kBins];      // first CTA: the row's counts up to and including a bin
   float cm[kBins];                    // and masses (estimated from the counts below the top bins)
   alignas(16) unsigned long long ent[THREADS];  // listed entries: order_key << 32 | ~index
   unsigned long long sorted[THREADS];
@@ -637,7 +638,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
   mine = warp_max(mine);
   if (lane == 0) S.red[warp] = __float_as_uint(mine);
   for (int i = t; i < kBins; i += THREADS) S.cnt[i] = 0;
-  if (t < kTopBins) S.mass[t] = 0;
+  for (int i = t; i < kTopBins; i += THREADS) S.mass[i] = 0;
   if (C > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   __syncthreads();
   const Slope c = slope_of(temp);
@@ -991,7 +992,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
     if (cmd.what == kCount) {
       if (cmd.fresh) {
         for (int i = t; i < kBins; i += THREADS) S.cnt[i] = 0;
-        if (t < kTopBins) S.mass[t] = 0;
+        for (int i = t; i < kTopBins; i += THREADS) S.mass[i] = 0;
         __syncthreads();
       }
       if (cmd.scale != 1.f)
@@ -1324,7 +1325,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
     cmd = S.cmd;
     if (cmd.what == kDone) return;
     if (cmd.what == kSlow) {
-      if (rank == 0) slow_row<T, THREADS>(a, row, S.tab, SlowScratch{S.red, S.ent, S.ties});
+      if (rank == 0) slow_row<T, THREADS>(a, row, S.tab, SlowScratch{S.red, reinterpret_cast<unsigned long long*>(S.cc), S.ties});
       return;
     }
     if (cmd.what == kWalk) break;
@@ -1412,13 +1413,16 @@ cudaError_t launch_sample(const Launch& L, const SampleFilteredArgs& a) {
   while (C < kMaxCluster && (static_cast<int64_t>(a.V) * sizeof(T) > 98304LL * C ||
                              (static_cast<int64_t>(a.rows) * C < 2 * L.num_sms && a.V > 2048 * C)))
     C *= 2;
-  // a thread for some 32 entries, 256 of them at least
-  const bool wide = a.V > 8192 * C;
-  const int threads = wide ? 512 : 256;
+  // A thread for some 32 entries, 256 of them at least; or 128, of which an SM holds eight CTAs
+  // and not four, for more rows of few entries than those hold (3000 rows of 300: 70.4 to 48.5
+  // us, of 1431: 89 to 79; of 4000: 112 to 119, and 25 rows of 1500: 18.6 to 20.4).
+  const int threads = a.V > 8192 * C ? 512 : a.V > kSmallVocab || a.rows <= 4 * L.num_sms ? 256 : 128;
   const int unit = threads * 16 / static_cast<int>(sizeof(T));  // a vector per thread
   const int slice = ((a.V + C - 1) / C + unit - 1) / unit * unit;
   const size_t smem = static_cast<size_t>(slice) * sizeof(T);
-  auto kernel = wide ? sample_filtered_kernel<T, 512> : sample_filtered_kernel<T, 256>;
+  auto kernel = threads == 512   ? sample_filtered_kernel<T, 512>
+                : threads == 256 ? sample_filtered_kernel<T, 256>
+                                 : sample_filtered_kernel<T, 128>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   return launch_kc(L, kernel, dim3(static_cast<unsigned>(a.rows) * C), dim3(threads), smem, C, a, C, slice);
