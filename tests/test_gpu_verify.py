@@ -696,6 +696,22 @@ def test_pages_and_sampling_replay():
         check_sampling(logits, 1, [1.0] * 3, [0, 30, 700], [0.9] * 3, None, u.tolist())
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [1, 35, 129, 1431, 2048])
+def test_sampling_many_small_rows(V, dtype):
+    """More rows of few entries than the GPU holds at once, every filter, some rows full of ties."""
+    g = torch.Generator(device="cuda").manual_seed(V)
+    times = 20
+    bs = len(GRID) * times
+    logits = 2.5 * torch.randn((bs * 4, V), generator=g, device="cuda")
+    logits[3::8] = logits[3::8].round()
+    logits = logits.to(torch.float32 if dtype == "f32" else torch.bfloat16)
+    k, p, mp = [x[0] for x in GRID] * times, [x[1] for x in GRID] * times, [x[2] for x in GRID] * times
+    temp = [0.4 + 0.01 * (i % 90) for i in range(bs)]
+    u = torch.rand(bs * 4, generator=g, device="cuda").tolist()
+    check_sampling(logits, 4, temp, k, p, mp, u)
+
+
 # ------------------------------------------------------------------ far offsets
 
 
