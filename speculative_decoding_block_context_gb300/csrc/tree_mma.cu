@@ -154,8 +154,13 @@ __device__ __forceinline__ bool warp_wait2(uint64_t* bar1, uint32_t parity1, uin
   if (__all_sync(0xffffffffu, one && two)) return true;
   return slow_wait(bar1, parity1, abort) && slow_wait(bar2, parity2, abort);
 }
+// 16 bytes from global to shared memory, and the wait for all that this thread has asked for.
+__device__ __forceinline__ void cp_async16(uint32_t dst, uint64_t src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 // 32 bytes (aligned so): whole sectors even where a warp's lanes write rows of their own.
-__device__ __forceinline__ void store32(float* p, const uint32_t* v) {
+__device__ __forceinline__ void store32(void* p, const uint32_t* v) {
   asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
                "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                : "memory");
@@ -438,6 +443,7 @@ __global__ void __launch_bounds__(MmaCfg<HD, MT>::THREADS, 1)
     // a negative scale's sign goes into Q; a scale of 0 stays apart from a hidden score's -inf
     const float k2 = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1e-30f);
     const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
+    const bool out32 = (reinterpret_cast<uint64_t>(a.out) & 31) == 0;  // (rows are multiples of 128 bytes)
     short* parent = s_parent[warp - 4];
     int n = 0, seq = 0, tree_b = -1;  // the lane's tiles so far, the CTA's
     int joins = 0, others = 0;        // lane 0: joins made, lane 1's tiles in them and in other items
@@ -461,31 +467,32 @@ __global__ void __launch_bounds__(MmaCfg<HD, MT>::THREADS, 1)
       q.q_row = static_cast<int64_t>(x.b) * a.width + q.node;
       return q;
     };
-    // An item's queries: asked for early, and put into shared memory once the products that
-    // read the item before's are done. Then its tree, if it reaches that.
-    struct Query {
-      uint4 v[HD / 8];
-    };
     auto q_of = [&](const Rows& q) {
       return reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + q.q_row * a.q_stride +
                                             static_cast<int64_t>(q.head) * HD);
     };
-    auto ask = [&](const Rows& q, Query& qv) {
-#pragma unroll
-      for (int x = 0; x < HD / 8; ++x) qv.v[x] = make_uint4(0, 0, 0, 0);
-      if (!q.loads || !q.live) return;
-      const uint4* src = q_of(q);
-#pragma unroll
-      for (int x = 0; x < HD / 8; ++x) qv.v[x] = __ldcg(src + x);
-    };
-    auto prepare = [&](const Walk<TM, TN>& x, const Rows& q, Query& qv) {
+    // An item's queries, once the products that read the item before's are done (a row's 16-byte
+    // pieces by lanes side by side, ROWS rows an instruction). Then its tree, if it reaches that.
+    constexpr int PIECES = HD / 8, ROWS = 32 / PIECES;
+    auto prepare = [&](const Walk<TM, TN>& x, const Rows& q) {
       if (q.loads) {
-        if (q.live) {
-          uint8_t* dst = sq + (q.own ? m : 0) * C::QTILE + row * 128;
+        const uint64_t mine = reinterpret_cast<uint64_t>(q_of(q));
+        int piece = lane;
+        asm volatile("" : "+r"(piece));  // (else what follows from it is kept in registers all along)
+        const int y = piece % PIECES;
+        uint8_t* dst = sq + (q.own ? m : 0) * C::QTILE + (y >> 3) * QHALF;
 #pragma unroll
-          for (int y = 0; y < HD / 8; ++y) {
-            qv.v[y].x ^= flip, qv.v[y].y ^= flip, qv.v[y].z ^= flip, qv.v[y].w ^= flip;
-            *reinterpret_cast<uint4*>(dst + (y >> 3) * QHALF + (((y & 7) ^ (row & 7)) * 16)) = qv.v[y];
+        for (int i = 0; i < PIECES; ++i) {
+          const int from = i * ROWS + piece / PIECES, r = quad * 32 + from;
+          const uint64_t src = __shfl_sync(0xffffffffu, mine, from) + y * 16;
+          if (r < q.rows) cp_async16(smem_u32(dst + r * 128 + (((y & 7) ^ (r & 7)) * 16)), src);
+        }
+        cp_async_wait();
+        if (flip) {
+          for (int i = 0; i < PIECES; ++i) {
+            const int r = quad * 32 + i * ROWS + piece / PIECES;
+            uint4* at = reinterpret_cast<uint4*>(dst + r * 128 + (((y & 7) ^ (r & 7)) * 16));
+            if (r < q.rows) *at = make_uint4(at->x ^ flip, at->y ^ flip, at->z ^ flip, at->w ^ flip);
           }
         }
         fence_async_smem();
@@ -509,10 +516,8 @@ __global__ void __launch_bounds__(MmaCfg<HD, MT>::THREADS, 1)
     bool more = w.next(a);
     Rows q{};
     if (more) {
-      Query qv;
       q = rows_for(w);
-      ask(q, qv);
-      prepare(w, q, qv);
+      prepare(w, q);
     }
     while (ok && more) {
       const bool own = q.own, live = q.live, warp_live = quad * 32 < q.rows;
@@ -617,15 +622,13 @@ __global__ void __launch_bounds__(MmaCfg<HD, MT>::THREADS, 1)
       const int tiles1 = own ? w.t1 - w.t0 : (w.t1 - w.t0) / 2;  // lane 1's tiles of the item
       // The next item's queries go in before this one's output comes out: its first scores run
       // meanwhile.
-      Query qv;
-      ask(q2, qv);
       if (!own && m == 1) {
         if (tiles1 > 0) {  // lane 0 joins the two outputs
           lane1_ml[row] = make_float2(mx, l);
           __syncwarp();
           if (lane == 0) mbar_arrive(&ml_ready);
         }
-        if (more) prepare(w2, q2, qv);
+        if (more) prepare(w2, q2);
         w = w2;
         q = q2;
         continue;
@@ -644,7 +647,7 @@ __global__ void __launch_bounds__(MmaCfg<HD, MT>::THREADS, 1)
         mx = to;
         __syncwarp();
       }
-      if (more) prepare(w2, q2, qv);
+      if (more) prepare(w2, q2);
       if (!(ok = warp_wait(&pv_done[m][(n - 1) & 1], ((n - 1) >> 1) & 1, ab))) break;
       if (join && !(ok = warp_wait(&pv_done[1][(others - 1) & 1], ((others - 1) >> 1) & 1, ab))) break;
       tc_fence_after();
@@ -673,15 +676,20 @@ __global__ void __launch_bounds__(MmaCfg<HD, MT>::THREADS, 1)
           if (!live) continue;
           if (w.whole) {
 #pragma unroll
-            for (int y = 0; y < 32; y += 8) {
-              uint32_t b[4];
+            for (int y = 0; y < 32; y += 16) {
+              uint32_t b[8];
 #pragma unroll
-              for (int z = 0; z < 4; ++z) {
+              for (int z = 0; z < 8; ++z) {
                 const __nv_bfloat162 b2 =
                     __floats2bfloat162_rn(__uint_as_float(o[y + 2 * z]), __uint_as_float(o[y + 2 * z + 1]));
                 b[z] = *reinterpret_cast<const uint32_t*>(&b2);
               }
-              *reinterpret_cast<uint4*>(dst + x + y) = make_uint4(b[0], b[1], b[2], b[3]);
+              if (out32) {
+                store32(dst + x + y, b);
+              } else {
+                *reinterpret_cast<uint4*>(dst + x + y) = make_uint4(b[0], b[1], b[2], b[3]);
+                *reinterpret_cast<uint4*>(dst + x + y + 8) = make_uint4(b[4], b[5], b[6], b[7]);
+              }
             }
           } else {
 #pragma unroll
