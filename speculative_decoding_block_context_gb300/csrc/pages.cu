@@ -12,6 +12,11 @@
 // so every CTA makes both sums itself (a few integers per request, from L2, scanned in
 // shared memory) rather than wait for another CTA's: no CTA reads what another one writes
 // (old columns are read from the table, new ones from the free list).
+//
+// Bound by latency: 128 requests of up to 17 tokens take 4.6 us in a graph (one request 4.1),
+// a launch and three dependent reads from L2. 557k tokens of 64 requests write 8.9 MB in 9.3
+// us: each thread searches its tokens' requests in shared memory, 2 CTAs per SM (1 CTA: 9.8,
+// 3: 11.9).
 
 #include <algorithm>
 #include <climits>

@@ -23,6 +23,16 @@
 // The passes over the row are bound by instructions (a row of 152k logits is 4.7k per warp
 // and instruction), so each is kept to what its row needs: a top-k row looks at few entries
 // twice, top-p adds an exponential each. Decisions are the first CTA's alone.
+//
+// What bounds it: the time one row takes, with as many rows in flight as shared memory holds
+// (76 of 152k bf16 logits: two CTAs of a cluster of four per SM). 1024 such rows: greedy 100 us
+// (3.1 TB/s), top-k 20 189, min-p 221, unfiltered 327, k = 1000 434, top-p 0.9 567. Of a top-p
+// row's 77k cycles (two CTAs sharing an SM) 7k load it, 20k count it (shared-memory atomics), 15k
+// sum its weights, and 25k are the first CTA's choices while the others wait.
+//
+// Tried and slower: a CTA per row that reads it again from L2 (the rows in flight do not stay
+// there); float64 or 64-bit shared-memory sums per bin; clusters of eight for these rows (k = 20:
+// 269 us); counting only what a histogram of vector maxima leaves (k = 1000: 469).
 
 #include <algorithm>
 #include <climits>
@@ -542,9 +552,7 @@ struct RowSmem {
   Command cmd;
 };
 
-// A cluster of C CTAs per row, each with `slice` of its entries in shared memory. (A CTA per row
-// that reads it again from L2 was slower: 1024 rows of 152k bf16 logits in flight two per SM
-// do not stay in L2.)
+// A cluster of C CTAs per row, each with `slice` of its entries in shared memory.
 template <typename T, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kernel(const SampleFilteredArgs a, int C, int slice) {
   constexpr int NW = THREADS / 32, VEC = 16 / sizeof(T);

