@@ -20,9 +20,9 @@
 // segment in which the draw falls (or the draw itself where the list starts at the top). That
 // segment's CTA walks it. Equal logits need no list: the border is a number of them.
 //
-// The passes over the row are bound by instructions (a row of 152k logits is 4.7k per warp
-// and instruction), so each is kept to what its row needs: a top-k row looks at few entries
-// twice, top-p adds an exponential each. Decisions are the first CTA's alone.
+// The passes over the row are bound by instructions, so each is kept to what its row needs: a
+// top-k row looks at few entries twice, top-p adds an exponential each. Decisions are the first
+// CTA's alone.
 //
 // What bounds it: the time one row takes, with as many rows in flight as shared memory holds
 // (76 of 152k bf16 logits: two CTAs of a cluster of four per SM). 1024 such rows: greedy 100 us
@@ -554,7 +554,8 @@ struct RowSmem {
 
 // A cluster of C CTAs per row, each with `slice` of its entries in shared memory.
 template <typename T, int THREADS>
-__global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kernel(const SampleFilteredArgs a, int C, int slice) {
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS)
+    sample_filtered_kernel(const SampleFilteredArgs a, int C, int slice) {
   constexpr int NW = THREADS / 32, VEC = 16 / sizeof(T);
   constexpr int kList = THREADS;  // entries the first CTA sorts, one per thread
   constexpr bool kExact = sizeof(T) == 2;
@@ -688,7 +689,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
           if (__fmul_rn(__fsub_rn(slice_top, l), per) < end) {
             const uint32_t pos = atomicAdd(&S.n_list, 1u);
             if (pos < kList)
-              S.ent[pos] = (static_cast<unsigned long long>(order_key(l)) << 32) | ~static_cast<uint32_t>(j0 + i * VEC + e);
+              S.ent[pos] =
+                  (static_cast<unsigned long long>(order_key(l)) << 32) | ~static_cast<uint32_t>(j0 + i * VEC + e);
           }
         });
       }
@@ -1261,7 +1263,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
           __syncthreads();
           const unsigned long long sum = S.left, draw = floor_part(u, sum);
           if (in > draw && in - v <= draw)
-            emit(static_cast<int>(~static_cast<uint32_t>(by >> 32)), ratio(key_value(static_cast<uint32_t>(S.sorted[at] >> 32)), sum));
+            emit(static_cast<int>(~static_cast<uint32_t>(by >> 32)),
+                 ratio(key_value(static_cast<uint32_t>(S.sorted[at] >> 32)), sum));
           cmd.what = kDone;
         } else {
           // the kept masses of the row's segments, and the one the draw falls in
@@ -1333,7 +1336,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_filtered_kerne
     cmd = S.cmd;
     if (cmd.what == kDone) return;
     if (cmd.what == kSlow) {
-      if (rank == 0) slow_row<T, THREADS>(a, row, S.tab, SlowScratch{S.red, reinterpret_cast<unsigned long long*>(S.cc), S.ties});
+      const SlowScratch scratch{S.red, reinterpret_cast<unsigned long long*>(S.cc), S.ties};
+      if (rank == 0) slow_row<T, THREADS>(a, row, S.tab, scratch);
       return;
     }
     if (cmd.what == kWalk) break;

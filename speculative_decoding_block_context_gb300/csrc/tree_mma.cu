@@ -667,7 +667,8 @@ __global__ void __launch_bounds__(MmaCfg<HD, MT>::THREADS, 1)
           f0 *= inv;
           f1 *= inv;
         }
-        const int64_t part = static_cast<int64_t>(2 * static_cast<int>(blockIdx.x) + (w.first_item ? 0 : 1)) * TM + (own ? m * 128 : 0) + row;
+        const int slot = 2 * static_cast<int>(blockIdx.x) + (w.first_item ? 0 : 1);
+        const int64_t part = static_cast<int64_t>(slot) * TM + (own ? m * 128 : 0) + row;
         __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + (q.q_row * a.nq + q.head) * HD;
 #pragma unroll
         for (int x = 0; x < HD; x += 32) {
@@ -756,7 +757,8 @@ int row_tiles_per_cta(int width, int group) { return width * group > 128 ? 2 : 1
 }  // namespace
 
 size_t tree_mma_bytes(int hd, int width, int group, int num_sms) {
-  return join_tasks_bytes(num_sms) + static_cast<size_t>(2 * num_sms) * 128 * row_tiles_per_cta(width, group) * (static_cast<size_t>(hd) * 4 + 8);
+  return join_tasks_bytes(num_sms) +
+         static_cast<size_t>(2 * num_sms) * 128 * row_tiles_per_cta(width, group) * (static_cast<size_t>(hd) * 4 + 8);
 }
 
 cudaError_t tree_mma(const Launch& L, TreeAttnArgs a, void* workspace) {
@@ -771,7 +773,8 @@ cudaError_t tree_mma(const Launch& L, TreeAttnArgs a, void* workspace) {
   if (!make_tmap_bf16(&kmap, a.keys, rows, a.hd, a.hd, box, &err) ||
       !make_tmap_bf16(&vmap, a.values, rows, a.hd, a.hd, box, &err))
     return cudaErrorInvalidValue;
-  if (a.hd == 64) return mt == 1 ? launch_mma<64, 1>(L, a, G, kmap, vmap, box) : launch_mma<64, 2>(L, a, G, kmap, vmap, box);
+  if (a.hd == 64)
+    return mt == 1 ? launch_mma<64, 1>(L, a, G, kmap, vmap, box) : launch_mma<64, 2>(L, a, G, kmap, vmap, box);
   return mt == 1 ? launch_mma<128, 1>(L, a, G, kmap, vmap, box) : launch_mma<128, 2>(L, a, G, kmap, vmap, box);
 }
 
