@@ -26,7 +26,7 @@
 //
 // What bounds it: the time one row takes, with as many rows in flight as shared memory holds
 // (76 of 152k bf16 logits: two CTAs of a cluster of four per SM). 1024 such rows: greedy 100 us
-// (3.1 TB/s), top-k 20 189, min-p 221, unfiltered 327, k = 1000 434, top-p 0.9 567. Of a top-p
+// (3.1 TB/s), top-k 20 190, min-p 222, unfiltered 318, k = 1000 428, top-p 0.9 547. Of a top-p
 // row's 77k cycles (two CTAs sharing an SM) 7k load it, 20k count it (shared-memory atomics), 15k
 // sum its weights, and 25k are the first CTA's choices while the others wait.
 //
@@ -812,14 +812,22 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
   // logit, place) for the others of a place below `past`, few.
   auto straight = [&](const uint4& v, float end, float past, float& low, auto f, auto g) {
     uint32_t others = 0;
+    const unsigned long long m2 = pack2(m, m), per2 = pack2(per, per), hi2 = pack2(-c.hi, -c.hi),
+                             lo2 = pack2(-c.lo, -c.lo), minus = pack2(-1.f, -1.f);
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      const float d = __fsub_rn(m, logit_of<T>(v, e)), pl = __fmul_rn(d, per);
-      f(e, pl);
-      const bool in = pl >= kTopBins && pl < end;
-      const float w = ex2_of(d, 0.f);
-      low += in ? w : 0.f;
-      if (!in && pl < past) others |= 1u << e;
+    for (int e = 0; e < VEC; e += 2) {
+      const unsigned long long d2 = fma2(pack2(logit_of<T>(v, e), logit_of<T>(v, e + 1)), minus, m2);
+      const float2 place2 = unpack2(mul2(d2, per2)), arg2 = unpack2(fma2(d2, hi2, mul2(d2, lo2)));
+      const float pl[2] = {place2.x, place2.y}, arg[2] = {arg2.x, arg2.y};
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        f(e + x, pl[x]);
+        const bool in = pl[x] >= kTopBins && pl[x] < end;
+        float w;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"(arg[x]));
+        low += in ? w : 0.f;
+        if (!in && pl[x] < past) others |= 1u << (e + x);
+      }
     }
     while (others) {
       const int e = __ffs(others) - 1;
