@@ -190,22 +190,29 @@ struct Walk {
   // The next item; false when the range is done.
   __device__ bool next(const TreeAttnArgs& a) {
     if (u1 - u <= (started ? start : 0)) return false;
-    while (r.n <= 0 || u - base >= static_cast<int64_t>(a.nkv) * mt * (nt + start)) {
-      base += r.n > 0 ? static_cast<int64_t>(a.nkv) * mt * (nt + start) : 0;
-      unsigned none = 0;
-      r = request_of(a, ++b, none);
-      enter(a);
+    int from = 0;
+    if (!started) {  // (the request holds the unit)
+      const int64_t local = u - base;
+      const int g = static_cast<int>(quotient(local, nt + start));
+      from = static_cast<int>(local - static_cast<int64_t>(g) * (nt + start));
+      head = g / mt;
+      tile_m = g - head * mt;
+    } else if (++tile_m == mt) {
+      tile_m = 0;
+      if (++head == a.nkv) {
+        head = 0;
+        base = u;
+        unsigned none = 0;
+        do r = request_of(a, ++b, none);
+        while (r.n <= 0);  // (units are left: some request holds them)
+        enter(a);
+      }
     }
-    const int64_t local = u - base;
-    const int g = static_cast<int>(quotient(local, nt + start));
-    const int from = static_cast<int>(local - static_cast<int64_t>(g) * (nt + start));
     const int to = static_cast<int>(min(static_cast<int64_t>(nt + start), from + (u1 - u)));
     if (to <= start) {  // (the range's only item)
       u = u1;
       return false;
     }
-    head = g / mt;
-    tile_m = g - head * mt;
     t0 = max(0, from - start);
     t1 = to - start;
     first_item = !started;

@@ -20,7 +20,7 @@
 //
 // What bounds it. Rows per lane (wide trees): the softmax warps, 1600 cycles of the 2290 that a
 // position tile takes a CTA (the tensor cores are busy for 1000): 128 trees of up to 64 nodes
-// over 512-8192 positions, 32 heads of 128, run in 516 us, 1141 TFLOP/s. Shared rows (narrow
+// over 512-8192 positions, 32 heads of 128, run in 489 us, 1205 TFLOP/s. Shared rows (narrow
 // trees): HBM, 32 trees of 16 nodes over the same in 96 us, 83% of the measured rate, four
 // requests' single tokens over 131072 positions in 320 us, 99%. One short request: latency, 15.4
 // us for 16 nodes over 2048 positions with the join.
@@ -434,6 +434,14 @@ __global__ void __launch_bounds__(MmaCfg<HD, MT>::THREADS, 1)
     const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
     const bool out32 = (reinterpret_cast<uint64_t>(a.out) & 31) == 0;  // (rows are multiples of 128 bytes)
     short* parent = s_parent[warp - 4];
+    // Wide trees: what this thread's node sees of the tree, by position tile from the context's
+    // last one on (the same for every head), and last of which request's tree and row tile that
+    // is. (Walked anew for every tile, 100 trees of 64 nodes over 10-500 positions took 128 us,
+    // not 94, and 128 over 512-8192 508, not 489. Narrow trees are walked: 108 of 9 nodes over
+    // 10-40 positions 42 us, with this 45.)
+    constexpr int kVis = MT == 2 ? (kTreeMaxWidth + TN - 2) / TN + 1 : 0;
+    uint64_t vis[kVis + 1];
+    vis[kVis] = ~0ull;
     int n = 0, seq = 0, tree_b = -1;  // the lane's tiles so far, the CTA's
     int joins = 0, others = 0;        // lane 0: joins made, lane 1's tiles in them and in other items
     bool ok = true;
@@ -495,11 +503,30 @@ __global__ void __launch_bounds__(MmaCfg<HD, MT>::THREADS, 1)
           mbar_arrive(&q1_ready);
         }
       }
-      if (a.tree_ids && x.t1 * TN > x.r.ctx && tree_b != x.b) {  // the item reaches the tree
+      if (!a.tree_ids || x.t1 * TN <= x.r.ctx) return;
+      if (tree_b != x.b) {  // the item reaches the tree
         __syncwarp();
         for (int i = lane; i < x.r.n; i += 32) parent[i] = static_cast<short>(i ? parent_of(a, x.b, i, err) : -1);
         __syncwarp();
         tree_b = x.b;
+      }
+      if constexpr (MT == 2) {
+        const uint64_t key = static_cast<uint64_t>(x.b) << 32 | (2 * x.tile_m + q.own);
+        if (!q.live || vis[kVis] == key) return;
+        vis[kVis] = key;
+        const int past = x.r.ctx % TN;  // context positions in the tree's first position tile
+        for (int s = 0; s <= (past + x.r.n - 1) / TN; ++s) vis[s] = 0;
+        int s = (past + q.node) / TN;
+        uint64_t word = 0;
+        for (int i = q.node; i >= 0; i = parent[i]) {  // ancestors only come earlier
+          if ((past + i) / TN != s) {
+            vis[s] = word;
+            word = 0;
+            s = (past + i) / TN;
+          }
+          word |= 1ull << ((past + i) % TN);
+        }
+        vis[s] = word;
       }
     };
     bool more = w.next(a);
@@ -543,12 +570,18 @@ __global__ void __launch_bounds__(MmaCfg<HD, MT>::THREADS, 1)
               see[x] = before >= 32 ? 0xffffffffu : before <= 0 ? 0u : (1u << before) - 1;
             }
             if (a.tree_ids && live && p0 + TN > w.r.ctx) {
-              for (int i = node; i >= 0; i = parent[i]) {
-                const int at = w.r.ctx + i - p0;
-                if (at < 0) break;  // ancestors only come earlier
+              if constexpr (MT == 2) {
+                const uint64_t word = vis[t - w.r.ctx / TN];
 #pragma unroll
-                for (int x = 0; x < TN / 32; ++x)
-                  if ((at >> 5) == x) see[x] |= 1u << (at & 31);
+                for (int x = 0; x < TN / 32; ++x) see[x] |= static_cast<uint32_t>(word >> (32 * x));
+              } else {
+                for (int i = node; i >= 0; i = parent[i]) {
+                  const int at = w.r.ctx + i - p0;
+                  if (at < 0) break;  // ancestors only come earlier
+#pragma unroll
+                  for (int x = 0; x < TN / 32; ++x)
+                    if ((at >> 5) == x) see[x] |= 1u << (at & 31);
+                }
               }
             }
 #pragma unroll
