@@ -22,7 +22,7 @@
 // position tile takes a CTA (the tensor cores are busy for 1000): 128 trees of up to 64 nodes
 // over 512-8192 positions, 32 heads of 128, run in 489 us, 1205 TFLOP/s. Shared rows (narrow
 // trees): HBM, 32 trees of 16 nodes over the same in 96 us, 83% of the measured rate, four
-// requests' single tokens over 131072 positions in 320 us, 99%. One short request: latency, 15.4
+// requests' single tokens over 131072 positions in 320 us, 99%. One short request: latency, 14.9
 // us for 16 nodes over 2048 positions with the join.
 //
 // Tried and slower: tiles of 128 positions; two threads per row (1384 us for the first shape
